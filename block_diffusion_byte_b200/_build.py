@@ -4,13 +4,17 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libbltdec.so")
-SOURCES = [os.path.join(PKG, "csrc", "engine.cu")]
 CSRC = os.path.join(PKG, "csrc")
-DEPS = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))] + [os.path.join(ROOT, "include", "bltdec.h")]
+INCLUDE = os.path.join(ROOT, "include")
+SOURCES = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cu")]
+DEPS = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))]
+DEPS += [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE)) if f.endswith(".h")]
 
 NVCC_FLAGS = [
     "-gencode",
@@ -42,10 +46,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libbltdec.so next to this file (skipped when up to date)."""
     if not force and not stale():
         return LIB
-    cmd = [nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp"] + SOURCES
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(s)[:-3] + ".o") for s in SOURCES]
+        compile_ = [f for f in NVCC_FLAGS if f != "-shared"] + ["-I", INCLUDE, "-c"]
+
+        def run(cmd):
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.run(cmd, check=True)
+
+        with ThreadPoolExecutor(max(1, min(len(SOURCES), os.cpu_count() or 1))) as pool:  # one nvcc per source
+            list(pool.map(lambda so: run([nvcc()] + compile_ + ["-o", so[1], so[0]]), zip(SOURCES, objs)))
+        run([nvcc()] + NVCC_FLAGS + ["-o", LIB + ".tmp"] + objs)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -1,4 +1,4 @@
-"""ctypes binding of the bltdec C ABI (include/bltdec.h): argument marshalling only.
+"""ctypes binding of the bltdec C ABI (include/bltdec.h, include/bltkv8.h): argument marshalling only.
 
 Every function keeps the C name and signature; device pointers are passed as
 torch CUDA tensors (or raw integers), host arrays as sequences of ints.  No
@@ -32,6 +32,11 @@ BLT_FLAG_TEST_STALL = 4  # test only: the persistent kernel's bounded waits must
 BLT_FLAG_TENSOR_CORES = 8  # passes of >= 128 rows: projections on the tcgen05 GEMM
 BLT_UNMASK_CONFIDENCE = 0
 BLT_UNMASK_EB = 1
+BLT_KV8_INT8 = 0
+BLT_KV8_E4M3 = 1
+BLT_T_F32 = 0
+BLT_T_BF16 = 1
+BLT_T_F16 = 2
 BLT_LAYER_NT = 12
 LAYER_ORDER = ("wq_c", "wk_c", "wv_c", "wo_c", "norm_c", "attn_norm", "wqkv", "wo", "ffn_norm", "w1", "w3", "w2")
 
@@ -53,6 +58,11 @@ EXPORTS = (
     "blt_dec_sync",
     "blt_dec_last_error",
     "blt_dec_free",
+    "blt_kv8_append",
+    "blt_kv8_read",
+    "blt_kv8_attend",
+    "blt_kv8_select",
+    "blt_kv8_last_error",
 )
 
 
@@ -123,6 +133,91 @@ class blt_dec_counters(C.Structure):
         return {k: int(getattr(self, k)) for k, _ in self._fields_}
 
 
+class blt_kv8_cache(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32),
+        ("n_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("page_tokens", C.c_int32),
+        ("n_pages", C.c_int32),
+        ("batch", C.c_int32),
+        ("max_pages", C.c_int32),
+        ("reserved", C.c_int32),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("k_exp", C.c_void_p),
+        ("v_exp", C.c_void_p),
+        ("page_stride", C.c_int64),
+        ("exp_stride", C.c_int64),
+        ("k_min", C.c_void_p),
+        ("k_max", C.c_void_p),
+        ("k_sexp", C.c_void_p),
+        ("sum_stride", C.c_int64),
+        ("sexp_stride", C.c_int64),
+        ("page_table", C.c_void_p),
+        ("status", C.c_void_p),
+    ]
+
+
+class blt_kv8_rows(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("dtype", C.c_int32),
+        ("n_rows", C.c_int32),
+        ("max_rows", C.c_int32),
+        ("reserved", C.c_int32),
+        ("row_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("row_offsets", C.c_void_p),
+        ("start", C.c_void_p),
+    ]
+
+
+class blt_kv8_attention(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p),
+        ("out", C.c_void_p),
+        ("lse", C.c_void_p),
+        ("dtype", C.c_int32),
+        ("n_q_heads", C.c_int32),
+        ("n_rows", C.c_int32),
+        ("max_rows", C.c_int32),
+        ("max_keys", C.c_int32),
+        ("scale", C.c_float),
+        ("q_row_stride", C.c_int64),
+        ("q_head_stride", C.c_int64),
+        ("out_row_stride", C.c_int64),
+        ("out_head_stride", C.c_int64),
+        ("row_offsets", C.c_void_p),
+        ("row_limit", C.c_void_p),
+        ("sel_pages", C.c_void_p),
+        ("sel_count", C.c_void_p),
+        ("n_select", C.c_int32),
+        ("reserved", C.c_int32),
+    ]
+
+
+class blt_kv8_selection(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p),
+        ("dtype", C.c_int32),
+        ("n_q_heads", C.c_int32),
+        ("n_rows", C.c_int32),
+        ("max_rows", C.c_int32),
+        ("max_keys", C.c_int32),
+        ("n_select", C.c_int32),
+        ("n_sink", C.c_int32),
+        ("n_local", C.c_int32),
+        ("q_row_stride", C.c_int64),
+        ("q_head_stride", C.c_int64),
+        ("row_offsets", C.c_void_p),
+        ("row_limit", C.c_void_p),
+        ("sel_pages", C.c_void_p),
+        ("sel_count", C.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -155,8 +250,15 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
     lib.blt_dec_last_error.restype = C.c_char_p
     lib.blt_dec_free.argtypes = [P]
     lib.blt_dec_free.restype = V
+    KP = C.POINTER(blt_kv8_cache)
+    lib.blt_kv8_append.argtypes = [KP, C.POINTER(blt_kv8_rows), P]
+    lib.blt_kv8_read.argtypes = [KP, C.POINTER(blt_kv8_rows), P]
+    lib.blt_kv8_attend.argtypes = [KP, C.POINTER(blt_kv8_attention), P]
+    lib.blt_kv8_select.argtypes = [KP, C.POINTER(blt_kv8_selection), P]
+    lib.blt_kv8_last_error.argtypes = []
+    lib.blt_kv8_last_error.restype = C.c_char_p
     for name in EXPORTS:
-        if name not in ("blt_dec_last_error", "blt_dec_free"):
+        if name not in ("blt_dec_last_error", "blt_dec_free", "blt_kv8_last_error"):
             getattr(lib, name).restype = C.c_int
     _lib = lib
     return lib
@@ -312,3 +414,169 @@ def blt_dec_last_error(h) -> str:
 def blt_dec_free(h) -> None:
     if h:
         load_library().blt_dec_free(h)
+
+
+# ----------------------------------------------------------------------------- 8-bit KV cache (bltkv8.h)
+_KV8_FORMAT = {"int8": BLT_KV8_INT8, "e4m3": BLT_KV8_E4M3, BLT_KV8_INT8: BLT_KV8_INT8, BLT_KV8_E4M3: BLT_KV8_E4M3}
+_TYPES = {"torch.float32": BLT_T_F32, "torch.bfloat16": BLT_T_BF16, "torch.float16": BLT_T_F16}
+
+
+def _kv8_type(t) -> int:
+    try:
+        return _TYPES[str(t.dtype)]
+    except KeyError:
+        raise ValueError(f"dtype {t.dtype}: float32, bfloat16 or float16 is wanted") from None
+
+
+def _want(t, name: str, dtype: str, ndim: int, device=None):
+    """`t` as an argument: a CUDA tensor of the type and rank, dense in its last axis."""
+    if t.dim() != ndim or str(t.dtype) not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: {ndim} axes of {dtype} are wanted, got {t.dim()} of {t.dtype}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name}: a tensor on {device or 'a CUDA device'} is wanted, got {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis has stride {t.stride(-1)}")
+    return t
+
+
+def _dense_from(t, name: str, axis: int):
+    """Raises unless the axes from `axis` on are contiguous."""
+    n = 1
+    for i in reversed(range(axis, t.dim())):
+        if t.shape[i] > 1 and t.stride(i) != n:
+            raise ValueError(f"{name}: axes from {axis} on have to be contiguous, strides are {tuple(t.stride())}")
+        n *= t.shape[i]
+    return t
+
+
+def kv8_cache(format, k, v, k_exp, v_exp, page_table, k_min=None, k_max=None, k_sexp=None, status=None) -> blt_kv8_cache:
+    """Describe an 8-bit paged KV cache held in torch tensors.
+
+    format ``"int8"`` or ``"e4m3"``; ``k``, ``v`` uint8 [n_pages, n_heads, page_tokens, head_dim]; ``k_exp``, ``v_exp`` uint8
+    [n_pages, n_heads, page_tokens / 16]; ``page_table`` int32 [batch, max_pages], contiguous; for
+    :func:`blt_kv8_select` also ``k_min``, ``k_max`` int8 [n_pages, n_heads, head_dim] and ``k_sexp`` uint8
+    [n_pages, n_heads]; ``status`` int32 [1].  The first axis may be strided (a layer's part of a larger
+    pool).  The struct keeps the tensors alive."""
+    if format not in _KV8_FORMAT:
+        raise ValueError(f"format {format!r}: 'int8' or 'e4m3' is wanted")
+    dev = k.device
+    _want(k, "k", "torch.uint8", 4)
+    n, h, pt, d = k.shape
+    for t, name, dtype, shape in ((v, "v", "torch.uint8", (n, h, pt, d)), (k_exp, "k_exp", "torch.uint8", (n, h, pt // 16)),
+                                  (v_exp, "v_exp", "torch.uint8", (n, h, pt // 16)), (k_min, "k_min", "torch.int8", (n, h, d)),
+                                  (k_max, "k_max", "torch.int8", (n, h, d)), (k_sexp, "k_sexp", "torch.uint8", (n, h))):
+        if t is not None and tuple(_want(t, name, dtype, len(shape), dev).shape) != shape:
+            raise ValueError(f"{name}: shape {shape} is wanted, got {tuple(t.shape)}")
+    for t, name in ((k, "k"), (v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp"), (k_min, "k_min"), (k_max, "k_max"), (k_sexp, "k_sexp")):
+        if t is not None:
+            _dense_from(t, name, 1)
+    for a, b, name in ((k, v, "k and v"), (k_exp, v_exp, "k_exp and v_exp"), (k_min, k_max, "k_min and k_max")):
+        if a is not None and b is not None and n > 1 and a.stride(0) != b.stride(0):
+            raise ValueError(f"{name}: page strides differ")
+    _dense_from(_want(page_table, "page_table", "torch.int32", 2, dev), "page_table", 0)
+    if status is not None:
+        _want(status, "status", "torch.int32", 1, dev)
+    stride = lambda t: 0 if t is None or n == 1 else t.stride(0)  # noqa: E731
+    c = blt_kv8_cache(_KV8_FORMAT[format], h, d, pt, n, page_table.shape[0], page_table.shape[1], 0, _ptr(k), _ptr(v), _ptr(k_exp),
+                      _ptr(v_exp), stride(k), stride(k_exp), _ptr(k_min), _ptr(k_max), _ptr(k_sexp), stride(k_min), stride(k_sexp),
+                      _ptr(page_table), _ptr(status))
+    c.keep = (k, v, k_exp, v_exp, page_table, k_min, k_max, k_sexp, status)
+    return c
+
+
+def kv8_rows(k, v, row_offsets, start, max_rows: int) -> blt_kv8_rows:
+    """Rows of keys and values: ``k``, ``v`` [n_rows, n_heads, head_dim] float32, bfloat16 or float16 with equal
+    strides; ``row_offsets`` int32 [batch + 1]; ``start`` int32 [batch]; ``max_rows``: most rows of one sequence."""
+    types = tuple(_TYPES)
+    _want(k, "k", types, 3)
+    _want(v, "v", types, 3, k.device)
+    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v differ in type, shape or strides")
+    _want(row_offsets, "row_offsets", "torch.int32", 1, k.device)
+    _want(start, "start", "torch.int32", 1, k.device)
+    if row_offsets.shape[0] != start.shape[0] + 1:
+        raise ValueError(f"row_offsets has {row_offsets.shape[0]} entries for {start.shape[0]} sequences")
+    r = blt_kv8_rows(_ptr(k), _ptr(v), _kv8_type(k), k.shape[0], int(max_rows), 0, k.stride(0), k.stride(1), _ptr(row_offsets), _ptr(start))
+    r.keep = (k, v, row_offsets, start)
+    r.shape = (start.shape[0], k.shape[1], k.shape[2])
+    return r
+
+
+def _kv8_q(q, row_offsets, row_limit):
+    _want(q, "q", tuple(_TYPES), 3)
+    _want(row_offsets, "row_offsets", "torch.int32", 1, q.device)
+    _want(row_limit, "row_limit", "torch.int32", 1, q.device)
+    if row_limit.shape[0] != q.shape[0]:
+        raise ValueError(f"row_limit has {row_limit.shape[0]} entries for {q.shape[0]} rows")
+
+
+def _kv8_sel(sel_pages, sel_count, q):
+    _dense_from(_want(sel_pages, "sel_pages", "torch.int32", 3, q.device), "sel_pages", 0)
+    _dense_from(_want(sel_count, "sel_count", "torch.int32", 2, q.device), "sel_count", 0)
+    if sel_pages.shape[:2] != sel_count.shape or sel_count.shape[0] != q.shape[0]:
+        raise ValueError(f"sel_pages {tuple(sel_pages.shape)} and sel_count {tuple(sel_count.shape)} for {q.shape[0]} rows")
+
+
+def kv8_attention(q, out, row_offsets, row_limit, max_rows: int, max_keys: int, scale: float, lse=None, sel_pages=None,
+                  sel_count=None) -> blt_kv8_attention:
+    """Attention of rows ``q`` [n_rows, n_q_heads, head_dim] into ``out`` (same type and shape): ``row_offsets`` int32
+    [batch + 1], ``row_limit`` int32 [n_rows]; ``max_rows``: most rows of one sequence, ``max_keys``: expected largest limit;
+    ``lse`` float32 [n_rows, n_q_heads]; ``sel_pages`` int32 [n_rows, n_heads, n_select] and ``sel_count`` int32
+    [n_rows, n_heads] limit the rows to pages (see :func:`blt_kv8_select`)."""
+    _kv8_q(q, row_offsets, row_limit)
+    _want(out, "out", str(q.dtype), 3, q.device)
+    if out.shape != q.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(q.shape)}")
+    if lse is not None and tuple(_dense_from(_want(lse, "lse", "torch.float32", 2, q.device), "lse", 0).shape) != tuple(q.shape[:2]):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}")
+    if (sel_pages is None) != (sel_count is None):
+        raise ValueError("sel_pages and sel_count come together")
+    n_select = 0
+    if sel_pages is not None:
+        _kv8_sel(sel_pages, sel_count, q)
+        n_select = sel_pages.shape[2]
+    a = blt_kv8_attention(_ptr(q), _ptr(out), _ptr(lse), _kv8_type(q), q.shape[1], q.shape[0], int(max_rows), int(max_keys), float(scale),
+                          q.stride(0), q.stride(1), out.stride(0), out.stride(1), _ptr(row_offsets), _ptr(row_limit), _ptr(sel_pages),
+                          _ptr(sel_count), n_select, 0)
+    a.keep = (q, out, row_offsets, row_limit, lse, sel_pages, sel_count)
+    a.shape = (row_offsets.shape[0] - 1, None if sel_pages is None else sel_pages.shape[1], q.shape[2])
+    return a
+
+
+def kv8_selection(q, row_offsets, row_limit, max_rows: int, max_keys: int, sel_pages, sel_count, n_sink: int = 0,
+                  n_local: int = 0) -> blt_kv8_selection:
+    """Choice of pages for rows ``q`` into ``sel_pages`` int32 [n_rows, n_heads, n_select] and ``sel_count`` int32 [n_rows, n_heads]."""
+    _kv8_q(q, row_offsets, row_limit)
+    _kv8_sel(sel_pages, sel_count, q)
+    s = blt_kv8_selection(_ptr(q), _kv8_type(q), q.shape[1], q.shape[0], int(max_rows), int(max_keys), sel_pages.shape[2], int(n_sink),
+                          int(n_local), q.stride(0), q.stride(1), _ptr(row_offsets), _ptr(row_limit), _ptr(sel_pages), _ptr(sel_count))
+    s.keep = (q, row_offsets, row_limit, sel_pages, sel_count)
+    s.shape = (row_offsets.shape[0] - 1, sel_pages.shape[1], q.shape[2])
+    return s
+
+
+def _kv8_call(name: str, cache: blt_kv8_cache, args, stream) -> None:
+    batch, heads, dim = args.shape
+    if batch != cache.batch or dim != cache.head_dim or heads not in (None, cache.n_heads):
+        raise ValueError(f"{name}: arguments for {batch} sequences, {heads} heads of {dim}; the cache has {cache.batch}, {cache.n_heads} of {cache.head_dim}")
+    lib = load_library()
+    rc = getattr(lib, name)(cache, args, stream)
+    if rc != BLT_OK:
+        raise BltError(rc, name, lib.blt_kv8_last_error().decode())
+
+
+def blt_kv8_append(cache: blt_kv8_cache, rows: blt_kv8_rows, stream: Optional[int] = None) -> None:
+    """``stream``: a cudaStream_t as an integer (``torch.cuda.current_stream().cuda_stream``); None or 0: the default stream."""
+    _kv8_call("blt_kv8_append", cache, rows, stream)
+
+
+def blt_kv8_read(cache: blt_kv8_cache, rows: blt_kv8_rows, stream: Optional[int] = None) -> None:
+    _kv8_call("blt_kv8_read", cache, rows, stream)
+
+
+def blt_kv8_attend(cache: blt_kv8_cache, attention: blt_kv8_attention, stream: Optional[int] = None) -> None:
+    _kv8_call("blt_kv8_attend", cache, attention, stream)
+
+
+def blt_kv8_select(cache: blt_kv8_cache, selection: blt_kv8_selection, stream: Optional[int] = None) -> None:
+    _kv8_call("blt_kv8_select", cache, selection, stream)
