@@ -30,6 +30,8 @@ BLT_FLAG_TIME_PASSES = 1
 BLT_FLAG_PERSISTENT = 2
 BLT_FLAG_TEST_STALL = 4  # test only: the persistent kernel's bounded waits must run out
 BLT_FLAG_TENSOR_CORES = 8  # passes of >= 128 rows: projections on the tcgen05 GEMM
+BLT_FLAG_KV8_INT8 = 16  # KV cache in 8 bits: int8 codes,
+BLT_FLAG_KV8_E4M3 = 32  # or e4m3 codes
 BLT_UNMASK_CONFIDENCE = 0
 BLT_UNMASK_EB = 1
 BLT_KV8_INT8 = 0

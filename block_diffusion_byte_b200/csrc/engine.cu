@@ -2,6 +2,7 @@
 // pool, latent cache, per-call sequencing of decoder passes, and the C ABI of
 // bltdec.h.  Every decoder step runs in the kernels of kernels.cuh.
 #include <algorithm>
+#include <climits>
 #include <mutex>
 #include <cmath>
 #include <cstdarg>
@@ -14,6 +15,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "bltdec.h"
+#include "bltkv8.h"
 #include "kernels.cuh"
 #include "mega.cuh"
 #include "tc_gemm.cuh"
@@ -73,6 +75,12 @@ struct blt_dec {
   float *rope_cos = nullptr, *rope_sin = nullptr;
   void* kv = nullptr;  // KV pool, element type per kv_f32
   int kv_f32 = 0;
+  // 8-bit KV cache (BLT_FLAG_KV8_*): codes [pages][L][2][H][PT][dh] in kv, their exponents, the pass's k and v rows
+  // and its rows per sequence
+  int kv8 = 0;
+  uint8_t* kv8_exp = nullptr;
+  float *k8 = nullptr, *v8 = nullptr;
+  int *span_off = nullptr, *span_start = nullptr;
   int* page_table = nullptr;
   std::vector<int> pt_host, free_pages, seq_npages;
   float* c_lat = nullptr;
@@ -501,22 +509,49 @@ int set_attn_attrs(blt_dec* h) {
   return BLT_OK;
 }
 
+// The self-attention of layer l on the 8-bit cache: the pass's k and v rows are stored, then its q rows attend.
+int attend_kv8(blt_dec* h, int l, int rows_ub, int seq_rows_ub, int keys_ub) {
+  blt_kv8_cache c{};
+  const size_t half = (size_t)h->H * h->PT * h->dh, ehalf = (size_t)h->H * (h->PT / 16);
+  c.format = h->kv8 == BLT_FLAG_KV8_INT8 ? BLT_KV8_INT8 : BLT_KV8_E4M3;
+  c.n_heads = h->H, c.head_dim = h->dh, c.page_tokens = h->PT, c.n_pages = h->n_pages;
+  c.batch = h->cfg.max_batch, c.max_pages = h->max_pages;
+  c.k = static_cast<uint8_t*>(h->kv) + (size_t)l * 2 * half, c.v = c.k + half;
+  c.k_exp = h->kv8_exp + (size_t)l * 2 * ehalf, c.v_exp = c.k_exp + ehalf;
+  c.page_stride = (int64_t)h->L * 2 * half, c.exp_stride = (int64_t)h->L * 2 * ehalf;
+  c.page_table = h->page_table;
+  c.status = h->sd.status;
+  blt_kv8_rows r{};
+  r.k = h->k8, r.v = h->v8, r.dtype = BLT_T_F32, r.n_rows = rows_ub, r.max_rows = seq_rows_ub;
+  r.row_stride = h->d, r.head_stride = h->dh, r.row_offsets = h->span_off, r.start = h->span_start;
+  blt_kv8_attention a{};
+  a.q = h->q, a.out = h->att, a.dtype = BLT_T_F32, a.n_q_heads = h->H, a.n_rows = rows_ub, a.max_rows = seq_rows_ub;
+  a.max_keys = keys_ub, a.scale = 1.0f / std::sqrt((float)h->dh);
+  a.q_row_stride = a.out_row_stride = h->d, a.q_head_stride = a.out_head_stride = h->dh;
+  a.row_offsets = h->span_off, a.row_limit = h->rows.nkeys;
+  int rc = blt_kv8_append(&c, &r, h->stream);
+  if (rc == BLT_OK) rc = blt_kv8_attend(&c, &a, h->stream);
+  return rc == BLT_OK ? BLT_OK : fail(h, rc, "layer %d: %s", l, blt_kv8_last_error());
+}
+
 // ---------------------------------------------------------------------------- one decoder pass
 // Runs every layer over the rows planned on the device (at most rows_ub rows,
 // keys below keys_ub, at most groups_ub attention groups).
-int run_pass_body(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int grp_rows_ub);
-// grp_rows_ub: rows per attention group at most (a sequence's rows in the pass, capped at
-// the planner's group size).
-int run_pass(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int grp_rows_ub = kAttnRows) {
-  return run_pass_body(h, rows_ub, keys_ub, groups_ub, want_head, std::min(grp_rows_ub, kAttnRows));
+int run_pass_body(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int seq_rows_ub);
+// seq_rows_ub: rows of one sequence in the pass at most.
+int run_pass(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int seq_rows_ub = INT_MAX) {
+  return run_pass_body(h, rows_ub, keys_ub, groups_ub, want_head, std::min(seq_rows_ub, rows_ub));
 }
-int run_pass_body(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int grp_rows_ub) {
+int run_pass_body(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want_head, int seq_rows_ub) {
   NvtxRange nvtx_("decoder pass (per-phase kernels)");
   const int d = h->d;
   // embed + per layer (cross add, attention partial + combine) + head statistics; GEMMs count themselves
-  h->launches += 1 + 3 * (unsigned long long)h->L + (want_head ? 1 : 0);
+  // (8-bit KV cache: append and attend in place of partial and combine, and the pass's spans)
+  h->launches += 1 + 3 * (unsigned long long)h->L + (want_head ? 1 : 0) + (h->kv8 ? 1 : 0);
+  const int grp_rows_ub = std::min(seq_rows_ub, kAttnRows);  // rows of one attention group at most
   const int nb = std::max(1, std::min(rows_ub, 1024));
   k_embed<<<nb, 256, 0, h->stream>>>(h->rows, h->embed, h->h, d);
+  if (h->kv8) k_row_spans<<<1, 256, 0, h->stream>>>(h->rows, h->cfg.max_batch, h->span_off, h->span_start);
   AttnArgs aa = attn_args(h);
   const int nchunks = std::max(1, (keys_ub + h->CH - 1) / h->CH);
   for (int l = 0; l < h->L; ++l) {
@@ -528,15 +563,21 @@ int run_pass_body(blt_dec* h, int rows_ub, int keys_ub, int groups_ub, bool want
     a.ldx = d;
     a.gain = h->attn_norm[l];
     a.q = h->q;
+    a.krow = h->k8;
+    a.vrow = h->v8;
     TRY(gemm<EPI_QKV>(h, h->qkv[l], a, rows_ub));
-    aa.layer = l;
-    launch_attn(h, dim3(h->H, nchunks, groups_ub), aa, grp_rows_ub);
-    const dim3 cg(rows_ub, h->H);
-    if (h->dh == 64) k_attn_combine<64><<<cg, 32, 0, h->stream>>>(aa);
-    else if (h->dh == 32) k_attn_combine<32><<<cg, 32, 0, h->stream>>>(aa);
-    else if (h->dh == 128) k_attn_combine<128><<<cg, 32, 0, h->stream>>>(aa);
-    else k_attn_combine<16><<<cg, 32, 0, h->stream>>>(aa);
-    CK(cudaGetLastError());
+    if (h->kv8) {
+      TRY(attend_kv8(h, l, rows_ub, seq_rows_ub, keys_ub));
+    } else {
+      aa.layer = l;
+      launch_attn(h, dim3(h->H, nchunks, groups_ub), aa, grp_rows_ub);
+      const dim3 cg(rows_ub, h->H);
+      if (h->dh == 64) k_attn_combine<64><<<cg, 32, 0, h->stream>>>(aa);
+      else if (h->dh == 32) k_attn_combine<32><<<cg, 32, 0, h->stream>>>(aa);
+      else if (h->dh == 128) k_attn_combine<128><<<cg, 32, 0, h->stream>>>(aa);
+      else k_attn_combine<16><<<cg, 32, 0, h->stream>>>(aa);
+      CK(cudaGetLastError());
+    }
     a = base_args(h);
     a.layer = l;
     a.X = h->att;
@@ -837,7 +878,7 @@ int mega_prepare_pd(blt_dec* h) {
 int mega_setup(blt_dec* h) {
   const int es = h->kv_f32 ? 4 : 2;
   const int nseg = h->F > kSegCols ? h->F / kSegCols : 1;
-  if (!(h->cfg.flags & BLT_FLAG_PERSISTENT) || h->d > 1024 || h->d % 128 != 0 || h->F % 128 != 0 || h->F > 4096 ||
+  if (!(h->cfg.flags & BLT_FLAG_PERSISTENT) || h->kv8 || h->d > 1024 || h->d % 128 != 0 || h->F % 128 != 0 || h->F > 4096 ||
       (h->F > kSegCols && h->F % kSegCols != 0) || (h->dh != 32 && h->dh != 64) || h->CH != 128 || 128 % h->PT != 0 ||
       2 * h->CH * h->dh * es > kSlotBytes)
     return BLT_OK;
@@ -1191,6 +1232,8 @@ int blt_dec_init(const blt_dec_config* cfg, const blt_dec_weights* w, void* cuda
   h->CH = c.attn_chunk > 0 ? c.attn_chunk : 128;
   if (h->CH > 128 || h->CH % 16) return bad("attn_chunk");
   h->CMAX = (c.max_ctx + h->CH - 1) / h->CH;
+  h->kv8 = c.flags & (BLT_FLAG_KV8_INT8 | BLT_FLAG_KV8_E4M3);
+  if (h->kv8 == (BLT_FLAG_KV8_INT8 | BLT_FLAG_KV8_E4M3) || (h->kv8 && (dhh < 32 || h->PT > 256))) return bad("8-bit KV cache");
 
   int rc = BLT_OK;
   auto run = [&]() -> int {
@@ -1266,12 +1309,13 @@ int blt_dec_init(const blt_dec_config* cfg, const blt_dec_weights* w, void* cuda
     h->weight_bytes_per_pass = h->head.bytes();
     for (int l = 0; l < L; ++l)
       h->weight_bytes_per_pass += h->qkv[l].bytes() + h->o[l].bytes() + h->w13[l].bytes() + h->w2[l].bytes();
-    h->kv_bytes_per_key = (unsigned long long)L * 2 * d * (pl == 2 ? 4 : 2);
-    // KV pool [pages][L][2][H][PT][dh]: bf16 for bf16 weights, fp32 for fp32 weights
+    // KV pool [pages][L][2][H][PT][dh]: codes with an 8-bit cache, else bf16 for bf16 weights, fp32 for fp32 weights
     h->kv_f32 = pl == 2;
+    const int kv_es = h->kv8 ? 1 : h->kv_f32 ? 4 : 2;
+    h->kv_bytes_per_key = (unsigned long long)L * 2 * d * kv_es + (h->kv8 ? (unsigned long long)L * 2 * h->H / 16 : 0);
     {
       char* kvp = nullptr;
-      TRY(dalloc(h, &kvp, (size_t)h->n_pages * L * 2 * d * h->PT * (h->kv_f32 ? 4 : 2)));
+      TRY(dalloc(h, &kvp, (size_t)h->n_pages * L * 2 * d * h->PT * kv_es));
       h->kv = kvp;
     }
     TRY(dalloc(h, &h->page_table, (size_t)c.max_batch * h->max_pages));
@@ -1287,6 +1331,13 @@ int blt_dec_init(const blt_dec_config* cfg, const blt_dec_weights* w, void* cuda
     TRY(dalloc(h, &h->rs, RL));
     TRY(dalloc(h, &h->q, (size_t)RL * d));
     TRY(dalloc(h, &h->att, (size_t)RL * d));
+    if (h->kv8) {
+      TRY(dalloc(h, &h->kv8_exp, (size_t)h->n_pages * L * 2 * h->H * (h->PT / 16)));
+      TRY(dalloc(h, &h->k8, (size_t)RL * d));
+      TRY(dalloc(h, &h->v8, (size_t)RL * d));
+      TRY(dalloc(h, &h->span_off, c.max_batch + 1));
+      TRY(dalloc(h, &h->span_start, c.max_batch));
+    }
     TRY(dalloc(h, &h->act, (size_t)RL * F));
     TRY(dalloc(h, &h->logits, (size_t)RL * 256));
     TRY(dalloc(h, &h->tmp, (size_t)R * L * d));
@@ -1414,6 +1465,7 @@ int blt_dec_prefill_noalloc(blt_dec_t* h, int batch, const blt_rows_in* rows, fl
       (size_t)h->L * h->d > (size_t)kNaRows * kNaMaxD)
     return fail(h, BLT_ERR_INVALID_ARG, "model exceeds the static prefill arena (d <= %d, d_ffn <= %d, heads <= %d, head dim <= %d, "
                 "attn_chunk %d, n_layers * d <= %d)", kNaMaxD, kNaMaxF, kNaMaxH, kNaMaxDh, kNaChunk, kNaRows * kNaMaxD);
+  if (h->kv8) return fail(h, BLT_ERR_INVALID_ARG, "the static prefill arena has no rows for an 8-bit KV cache");
   TRY(check_pending(h, rows, true));
   CallDesc cd;
   TRY(make_desc(h, batch, rows->row_offsets, rows->latent_offsets, cd));

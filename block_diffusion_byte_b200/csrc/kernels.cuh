@@ -111,6 +111,7 @@ struct GemmArgs {
   const int* row_byte;
   const float* rope_cos;  // [max_ctx][dh/2], or [row][dh/2] when rope_by_row
   const float* rope_sin;
+  float *krow, *vrow;     // 8-bit KV cache: k and v of row r go to krow / vrow + r * d instead (NULL: into the pool)
   int rope_by_row;      // rope tables indexed by activation row (per-pass copy) instead of position
   const int* row_page;  // KV page of each row's position (-1: none); NULL: look up page_table
   // EPI_LATC
@@ -220,6 +221,12 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs& a, int mt, int r16
         q[j + half] = o1;
         return;
       }
+      if (a.krow) {
+        float* k = a.krow + (size_t)row * a.d + h * a.dh;
+        k[j] = o0;
+        k[j + half] = o1;
+        return;
+      }
       const int page = row_kv_page(a, row, seq, pos);
       if (page < 0) {
         set_status(a.status, kErrDevice);
@@ -228,12 +235,17 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs& a, int mt, int r16
       kv_store(a, kv_offset(a, page, a.layer, 0, h, pos % a.PT, kv_dim(a, pos, j)), o0);
       kv_store(a, kv_offset(a, page, a.layer, 0, h, pos % a.PT, kv_dim(a, pos, j + half)), o1);
     } else {
+      const int n0 = lt * 16 + r16, n1 = n0 + 8;
+      if (a.krow) {
+        a.vrow[(size_t)row * a.d + n0] = v0;
+        a.vrow[(size_t)row * a.d + n1] = v1;
+        return;
+      }
       const int page = row_kv_page(a, row, seq, pos);
       if (page < 0) {
         set_status(a.status, kErrDevice);
         return;
       }
-      const int n0 = lt * 16 + r16, n1 = n0 + 8;
       kv_store(a, kv_offset(a, page, a.layer, 1, n0 / a.dh, pos % a.PT, kv_dim(a, pos, n0 % a.dh)), v0);
       kv_store(a, kv_offset(a, page, a.layer, 1, n1 / a.dh, pos % a.PT, kv_dim(a, pos, n1 % a.dh)), v1);
     }
@@ -1335,6 +1347,22 @@ __device__ void plan_rows(const PlanArgs& p, int B, const int* row_off, const in
 __global__ void __launch_bounds__(256) k_plan(PlanArgs p, CallDesc cd, SeqDev sd, RowsDev rd) {
   __shared__ int sh[3 * (kMaxCallBatch + 1)];
   plan_rows(p, cd.batch, cd.row_off, cd.lat_off, sd, rd, threadIdx.x, blockDim.x, sh, [] { __syncthreads(); });
+}
+
+// The rows of each sequence in the planned pass, for the 8-bit KV cache: off[s] .. off[s + 1] - 1 (rows are in
+// sequence order) at positions start[s], start[s] + 1, ...
+__global__ void __launch_bounds__(256) k_row_spans(RowsDev rd, int batch, int* off, int* start) {
+  const int n = *rd.n_rows;
+  for (int s = threadIdx.x; s <= batch; s += blockDim.x) {
+    int lo = 0, hi = n;  // the first row of a sequence >= s
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (rd.seq[mid] < s) lo = mid + 1;
+      else hi = mid;
+    }
+    off[s] = lo;
+    if (s < batch) start[s] = lo < n ? rd.pos[lo] : 0;
+  }
 }
 
 // Latent rows: new latent j of sequence s goes to slot n_lat[s] + (j - lat_off[s]).

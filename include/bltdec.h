@@ -107,6 +107,12 @@ typedef struct {
                                    (QKV, O, SwiGLU, W2, head) on the tcgen05 GEMM (bf16 weights only).
                                    Results then agree with the GEMV path to rounding, not bit for bit.
                                    Costs a second, row-major bf16 copy of those weights. */
+#define BLT_FLAG_KV8_INT8 16 /* keep the KV cache in 8 bits: int8 codes (bltkv8.h) with one scale per 16 positions and */
+#define BLT_FLAG_KV8_E4M3 32 /* head, or e4m3 codes.  One of the two at most; head dim 32, 64 or 128, page_tokens <= 256.
+                                K/V then take a half (bf16 weights) or a quarter (fp32) of their bytes.  Every pass runs on
+                                the per-phase kernels (BLT_FLAG_PERSISTENT is ignored) and blt_dec_prefill_noalloc is
+                                refused.  A cached position can lose low bits when rows that share its 16 positions are
+                                stored later (drafts and block rows included): see blt_kv8_append. */
 
 typedef struct {
   const float *embed;      /* host [vocab, d] */

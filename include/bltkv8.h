@@ -1,6 +1,7 @@
 /*
  * bltkv8.h -- C ABI of the 8-bit paged KV cache: storing, attention over it, and attention over
- * selected pages of it (sm_100a).  Part of libbltdec.so.
+ * selected pages of it (sm_100a).  Part of libbltdec.so; the decoder engine of bltdec.h uses the same
+ * calls in a handle with BLT_FLAG_KV8_INT8 or BLT_FLAG_KV8_E4M3.
  *
  * Cache.  Keys and values are 8-bit codes in pages of page_tokens positions; a page table gives each
  * sequence's pages.  Every 16 positions of one head (a "block") share one exponent byte e, one for
