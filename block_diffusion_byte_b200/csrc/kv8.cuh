@@ -143,6 +143,21 @@ __device__ __forceinline__ void kv8_st(void* p, int dtype, long long i, float v)
   else if (dtype == BLT_T_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
+// Four elements from i; vec: 16-byte aligned rows (i a multiple of 4).
+__device__ __forceinline__ void kv8_ld4(const void* p, int dtype, long long i, bool vec, float (&x)[4]) {
+  if (!vec) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = kv8_ld(p, dtype, i + j);
+  } else if (dtype == BLT_T_F32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  } else {
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+    const float2 f = dtype == BLT_T_BF16 ? bf16x2_to_f2(a.x) : __half22float2(*reinterpret_cast<const __half2*>(&a.x));
+    const float2 h = dtype == BLT_T_BF16 ? bf16x2_to_f2(a.y) : __half22float2(*reinterpret_cast<const __half2*>(&a.y));
+    x[0] = f.x, x[1] = f.y, x[2] = h.x, x[3] = h.y;
+  }
+}
 // Eight elements from i; vec: 16-byte aligned.
 __device__ __forceinline__ void kv8_ld8(const void* p, int dtype, long long i, bool vec, float (&x)[8]) {
   if (!vec) {

@@ -9,8 +9,14 @@
 //     reads 16-byte pieces;
 //   V^T (A operand): a lane holds, for keys 2t, 2t+1, 2t+8, 2t+9, its eighth g of the channels; the byte
 //     permute that spreads codes for conversion also pairs two keys, so the transpose costs nothing.
-// No shared memory and no barrier stands between memory and the tensor cores; each warp takes 16-key units
-// of its own with its own running maximum and sum, the next units' loads in flight while it computes.
+// Codes become f16: both formats are exact in it (int8: 1024 + 128 + c read off the byte, less 1152; e4m3: the
+// converter), and a two-plane f16 operand has 22 bits where bf16 has 16.  f16's range is met by powers of two:
+// each query is scaled so that its largest channel lies in [2^14, 2^15), and weights times their block's scale are
+// taken relative to the largest block scale so far (times 2^14).  What lies 2^38 below the largest is cut.
+//
+// Each warp takes 16-key units of its own with its own running maximum and sum, and copies them (cp.async)
+// through a ring of its own in shared memory, kKv8Stages - 1 steps ahead: no barrier stands between the warps, and
+// the bytes in flight (two CTAs of eight warps, 8 KB each ahead: 128 KB an SM) cover the memory's latency.
 // Warps are joined in shared memory, and the CTAs that split a long key axis (a cluster) over distributed
 // shared memory, in a fixed order: no workspace, no second launch, no atomics.
 #pragma once
@@ -42,22 +48,6 @@ __device__ __forceinline__ int kv8_vdim(int b, int g) {
   return (b / VB) * 8 * VB + g * VB + b % VB;
 }
 
-__device__ __forceinline__ uint32_t ldg_u32(const uint8_t* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 ldg_u64(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint4 ldg_u128(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 template <int DH>
 __device__ __forceinline__ void kv8_load_krow(uint32_t (&w)[DH / 16], const uint8_t* row, int t) {
   constexpr int CB = kv8_kpiece<DH>();
@@ -65,10 +55,10 @@ __device__ __forceinline__ void kv8_load_krow(uint32_t (&w)[DH / 16], const uint
   for (int i = 0; i < DH / 16; i += CB / 4) {
     const uint8_t* p = row + kv8_kdim<DH>(i, t);
     if constexpr (CB == 16) {
-      const uint4 x = ldg_u128(p);
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
       w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
     } else {
-      const uint2 x = ldg_u64(p);
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
       w[i] = x.x, w[i + 1] = x.y;
     }
   }
@@ -77,14 +67,14 @@ template <int DH>
 __device__ __forceinline__ void kv8_load_vrow(uint32_t (&w)[DH / 32], const uint8_t* row, int g) {
   constexpr int VB = kv8_vpiece<DH>();
   if constexpr (VB == 16) {
-    const uint4 x = ldg_u128(row + g * 16);
+    const uint4 x = *reinterpret_cast<const uint4*>(row + g * 16);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   } else if constexpr (VB == 8) {
-    const uint2 x = ldg_u64(row + g * 8);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + g * 8);
     w[0] = x.x, w[1] = x.y;
   } else {
 #pragma unroll
-    for (int j = 0; j < DH / 32; ++j) w[j] = ldg_u32(row + j * 32 + g * 4);
+    for (int j = 0; j < DH / 32; ++j) w[j] = *reinterpret_cast<const uint32_t*>(row + j * 32 + g * 4);
   }
 }
 
@@ -99,33 +89,84 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// P planes of two fp32 values as packed bf16: the sum of the planes has 8 P bits of the value.
+// P planes of two fp32 values as packed f16: the sum of the planes has 11 P bits of the value (|x| < 65504).
 template <int P>
 __device__ __forceinline__ void kv8_planes(float x0, float x1, uint32_t (&pl)[P]) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    pl[i] = f2_to_bf16x2(x0, x1);
+    const __half2 h = __floats2half2_rn(x0, x1);
+    pl[i] = *reinterpret_cast<const uint32_t*>(&h);
     if (i + 1 < P) {
-      const float2 f = bf16x2_to_f2(pl[i]);
+      const float2 f = __half22float2(h);
       x0 -= f.x, x1 -= f.y;
     }
   }
 }
 
+// The four codes of word w as f16: channels 0, 1 and 2, 3.
+template <int FMT>
+__device__ __forceinline__ uint2 kv8_half4(uint32_t w) {
+  uint2 d;
+  if constexpr (FMT == 0) {
+    const uint32_t x = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d.x) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d.y) : "r"(b), "r"(0x64806480u));
+  } else {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n" : "=r"(d.x), "=r"(d.y) : "r"(w));
+  }
+  return d;
+}
+// Codes 2 j and 2 j + 1 of words a and b as f16 pairs (a's in the lower half): channel 2 j, channel 2 j + 1.
+template <int FMT>
+__device__ __forceinline__ uint2 kv8_half_pairs(uint32_t a, uint32_t b, int j) {
+  uint2 d;
+  if constexpr (FMT == 0) {
+    const uint32_t x = (__byte_perm(a, b, j ? 0x0602 : 0x0400) & 0x00ff00ffu) ^ 0x64806480u;
+    const uint32_t y = (__byte_perm(a, b, j ? 0x0703 : 0x0501) & 0x00ff00ffu) ^ 0x64806480u;
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d.x) : "r"(x), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(d.y) : "r"(y), "r"(0x64806480u));
+    return d;
+  } else {
+    return kv8_half4<1>(__byte_perm(a, b, j ? 0x7362 : 0x5140));
+  }
+}
+
+// D += A(16x16, f16, row) * B(16x8, f16, col), fp32 accumulate.
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+constexpr int kKv8Stages = 3;
+template <int DH>
+__host__ __device__ constexpr int kv8_units() { return DH <= 64 ? 2 : 1; }  // units per step: 4 KB (2 KB for DH 32)
+
 template <int DH, int NQ>
 struct Kv8Smem {
   static constexpr int OS = DH + 4;  // row stride of a partial output (floats): breaks bank alignment of the rows
-  float o[kKv8Warps][8 * NQ][OS];
+  union {
+    uint8_t ring[kKv8Warps][kKv8Stages][kv8_units<DH>()][2][kKv8Block * DH];
+    float o[kKv8Warps][8 * NQ][OS];
+  };
+  int2 meta[kKv8Warps][kKv8Stages][kv8_units<DH>()];  // position and exponents (keys' | values' << 8) of a staged unit
   float m[kKv8Warps][8 * NQ], l[kKv8Warps][8 * NQ];
   float bo[8 * NQ][OS];  // the CTA's own sums, read by the cluster
   float bm[8 * NQ], bl[8 * NQ];
 };
 
+// Registers decide the CTAs an SM holds: two where a lane's queries and outputs leave room.
+template <int DH, int QP, int NQ>
+__host__ __device__ constexpr int kv8_ctas() { return NQ * (DH / 16) * (2 * QP + 4) <= 64 ? 2 : 1; }
+
 // grid (tiles x CL, key/value heads, sequences), clusters of CL along x.
 template <int DH, int FMT, int QP, int PP, int NQ>
-__global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a,
+__global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_attend(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a,
                                                                 const int CL) {
-  constexpr int U = DH <= 64 ? 2 : 1;  // units per step of a warp
+  constexpr int U = kv8_units<DH>(), S = kKv8Stages;
   constexpr int KW = DH / 16, VW = DH / 32, MT = DH / 16;
   extern __shared__ float4 kv8_smem4[];
   Kv8Smem<DH, NQ>& sm = *reinterpret_cast<Kv8Smem<DH, NQ>*>(kv8_smem4);
@@ -166,30 +207,6 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) lim[n][e] = __shfl_sync(0xffffffffu, lim_n, n * 8 + 2 * t + e);
 
-  // query fragments (B operand): k16 step i holds the channels of key byte group i
-  uint32_t qf[NQ][KW][2][QP];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int qn = n * 8 + g;
-    const long long base = qn < nq ? (long long)row_of(qn) * a.qs + (long long)head_of(qn) * a.qhs : 0;
-#pragma unroll
-    for (int i = 0; i < KW; ++i) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (qn < nq) {
-        const long long at = base + kv8_kdim<DH>(i, t);
-        if (a.q_vec && a.dtype == BLT_T_F32) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
-          x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = kv8_ld(a.q, a.dtype, at + j);
-        }
-      }
-      kv8_planes<QP>(x[0], x[1], qf[n][i][0]);
-      kv8_planes<QP>(x[2], x[3], qf[n][i][1]);
-    }
-  }
-
   // this CTA's units: [u0, u1) of nu, its warps taking steps of U units in turn
   const int* list = nullptr;
   int nu = (maxlim + kKv8Block - 1) / kKv8Block;
@@ -202,7 +219,95 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
   const int u0 = min(rank * per, nu), u1 = min(nu, u0 + per);
   const int steps = max(0, (u1 - u0 + U - 1) / U - warp + kKv8Warps - 1) / kKv8Warps;
 
+  // pages, positions and exponents of the warp's next 32 units, one per lane
+  int c_page = -1, c_pos = kKv8NoPos, c_ex = 0;
+  auto resolve = [&](int it0) {
+    const int u = u0 + (warp + kKv8Warps * (it0 + lane / U)) * U + lane % U;
+    c_page = -1;
+    c_pos = kKv8NoPos;
+    c_ex = 127;
+    if (it0 + lane / U >= steps || u >= u1) return;
+    const int e = kv8_div_tpp(c, u), sub = u - e * c.tpp;
+    int pl = e;
+    if (sel) {
+      pl = __ldg(list + e);
+      const int prev = e > 0 ? __ldg(list + e - 1) : -1;
+      if (pl < 0 || pl <= prev || pl >= c.max_pages) return;
+    }
+    const int pos = pl * c.PT + sub * kKv8Block;
+    if (pos >= maxlim) return;
+    c_page = kv8_page(c, s, pl);
+    if (c_page < 0) return;
+    c_pos = pos;
+    const size_t ex = (size_t)c_page * c.exp_stride + kvh * c.tpp + sub;
+    c_ex = __ldg(c.ke + ex) | __ldg(c.ve + ex) << 8;
+  };
+  constexpr int PER = 32 / U;  // steps per resolve
+  auto issue = [&](int it, int slot) {  // copies of step `it`
+    if (it < steps) {
+      if (it % PER == 0) resolve(it);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int src = (it * U + u) & 31;
+        const int page = __shfl_sync(0xffffffffu, c_page, src), pos = __shfl_sync(0xffffffffu, c_pos, src);
+        if (page < 0) continue;
+        const int blk = pos / kKv8Block, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
+        const size_t at = (size_t)page * c.page_stride + ((size_t)kvh * c.PT + sub * kKv8Block) * DH;
+        uint8_t* dst = sm.ring[warp][slot][u][0];
+#pragma unroll
+        for (int i = lane; i < DH; i += 32) {
+          cp_async16(dst + i * 16, c.k + at + i * 16, 16);
+          cp_async16(dst + kKv8Block * DH + i * 16, c.v + at + i * 16, 16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  auto note = [&](int it, int slot) {  // what the copies of step `it` are
+    if (it >= steps) return;
+    const int src = (it * U + lane) & 31;
+    const int pos = __shfl_sync(0xffffffffu, c_pos, src), ex = __shfl_sync(0xffffffffu, c_ex, src);
+    if (lane < U) sm.meta[warp][slot][lane] = make_int2(pos, ex);
+  };
+  for (int i = 0; i < S - 1; ++i) issue(i, i);
+  for (int i = 0; i < S - 1; ++i) note(i, i);
+
+  // query fragments (B operand): k16 step i holds the channels of key byte group i.  A query is scaled by a power
+  // of two; `qs` undoes it for queries 2t and 2t + 1, times the scale and log2 e: scores are in units of log 2.
+  uint32_t qf[NQ][KW][2][QP];
+  float qs[NQ][2];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    const int qn = n * 8 + g;
+    const long long base = qn < nq ? (long long)row_of(qn) * a.qs + (long long)head_of(qn) * a.qhs : 0;
+    float x[KW][4];
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < KW; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+      if (qn < nq) {
+        const long long at = base + kv8_kdim<DH>(i, t);
+        kv8_ld4(a.q, a.dtype, at, a.q_vec, x[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(x[i][j]));
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const int ex = max((int)(__float_as_uint(big) >> 23), 15);
+    const float up = kv8_pow2(268 - ex), down = kv8_pow2(ex - 14);
+#pragma unroll
+    for (int i = 0; i < KW; ++i) {
+      kv8_planes<QP>(x[i][0] * up, x[i][1] * up, qf[n][i][0]);
+      kv8_planes<QP>(x[i][2] * up, x[i][3] * up, qf[n][i][1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * (a.scale * 1.4426950408889634f);
+  }
+
   float m[NQ][2], l[NQ][2], o[MT][NQ][4];
+  int vref = kKv8LowExp;  // the largest value exponent so far; outputs are in units of 2^(vref - 127 - 14)
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n][0] = m[n][1] = -INFINITY;
@@ -213,92 +318,44 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
       for (int e = 0; e < 4; ++e) o[j][n][e] = 0.f;
   }
 
-  // pages and positions of the warp's next 32 units, one per lane
-  int c_page = -1, c_pos = kKv8NoPos;
-  auto resolve = [&](int it0) {
-    const int u = u0 + (warp + kKv8Warps * (it0 + lane / U)) * U + lane % U;
-    c_page = -1;
-    c_pos = kKv8NoPos;
-    if (it0 + lane / U >= steps || u >= u1) return;
-    const int e = kv8_div_tpp(c, u);
-    int pl = e, pos = u * kKv8Block;
-    if (sel) {
-      pl = __ldg(list + e);
-      const int prev = e > 0 ? __ldg(list + e - 1) : -1;
-      if (pl < 0 || pl <= prev || pl >= c.max_pages) return;
-      pos = pl * c.PT + (u - e * c.tpp) * kKv8Block;
-      if (pos >= maxlim) return;
-    }
-    c_page = kv8_page(c, s, pl);
-    if (c_page >= 0) c_pos = pos;
-  };
-
-  struct Stage {
-    uint32_t k[U][2][KW], v[U][4][VW];
-    int pos[U];
-    uint32_t ke[U], ve[U];
-  };
-  auto load = [&](Stage& st, int it) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int src = (it * U + u) & 31;
-      const int page = __shfl_sync(0xffffffffu, c_page, src), pos = __shfl_sync(0xffffffffu, c_pos, src);
-      st.pos[u] = pos;
-      if (page < 0) {
-        st.ke[u] = st.ve[u] = 127;
-#pragma unroll
-        for (int i = 0; i < KW; ++i) st.k[u][0][i] = st.k[u][1][i] = 0;
-#pragma unroll
-        for (int i = 0; i < VW; ++i) st.v[u][0][i] = st.v[u][1][i] = st.v[u][2][i] = st.v[u][3][i] = 0;
-        continue;
-      }
-      const int blk = pos / kKv8Block, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
-      const size_t at = (size_t)page * c.page_stride + ((size_t)kvh * c.PT + sub * kKv8Block) * DH;
-      const size_t ex = (size_t)page * c.exp_stride + kvh * c.tpp + sub;
-      const uint8_t *kp = c.k + at, *vp = c.v + at;
-      kv8_load_krow<DH>(st.k[u][0], kp + g * DH, t);
-      kv8_load_krow<DH>(st.k[u][1], kp + (g + 8) * DH, t);
-      kv8_load_vrow<DH>(st.v[u][0], vp + (2 * t) * DH, g);
-      kv8_load_vrow<DH>(st.v[u][1], vp + (2 * t + 1) * DH, g);
-      kv8_load_vrow<DH>(st.v[u][2], vp + (2 * t + 8) * DH, g);
-      kv8_load_vrow<DH>(st.v[u][3], vp + (2 * t + 9) * DH, g);
-      st.ke[u] = __ldg(c.ke + ex);
-      st.ve[u] = __ldg(c.ve + ex);
-    }
-  };
-
-  const float cs = a.scale * 1.4426950408889634f;  // scores in units of log 2
-  auto compute = [&](const Stage& st) {
+  auto compute = [&](int slot) {
     float sc[U][NQ][4];
+    int pos[U], ve[U];
+    int vmax = vref;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int2 meta = sm.meta[warp][slot][u];
+      pos[u] = meta.x;
+      ve[u] = meta.y >> 8;
+      vmax = max(vmax, ve[u]);
+      const uint8_t* kp = sm.ring[warp][slot][u][0];
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[u][n][e] = 0.f;
+      uint32_t k0[KW], k1[KW];
+      kv8_load_krow<DH>(k0, kp + g * DH, t);
+      kv8_load_krow<DH>(k1, kp + (g + 8) * DH, t);
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        uint4 f;
-        f.x = kv8_pair<FMT>(st.k[u][0][i], 0, kv8_sel<FMT>(0, 1));
-        f.y = kv8_pair<FMT>(st.k[u][1][i], 0, kv8_sel<FMT>(0, 1));
-        f.z = kv8_pair<FMT>(st.k[u][0][i], 0, kv8_sel<FMT>(2, 3));
-        f.w = kv8_pair<FMT>(st.k[u][1][i], 0, kv8_sel<FMT>(2, 3));
+        const uint2 x = kv8_half4<FMT>(k0[i]), y = kv8_half4<FMT>(k1[i]);
+        const uint4 f = make_uint4(x.x, y.x, x.y, y.y);
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int p = QP - 1; p >= 0; --p) mma16816(sc[u][n], f, qf[n][i][0][p], qf[n][i][1][p]);
+          for (int p = QP - 1; p >= 0; --p) mma16816_f16(sc[u][n], f, qf[n][i][0][p], qf[n][i][1][p]);
       }
-      const float ks = kv8_pow2(st.ke[u]) * cs;
-      const bool whole = st.pos[u] + kKv8Block <= minlim;
+      const float ks = kv8_pow2(meta.y & 0xff);
+      const bool whole = pos[u] + kKv8Block <= minlim;
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc[u][n][e] *= ks;
-          if (!whole && st.pos[u] + g + (e >> 1) * 8 >= lim[n][e & 1]) sc[u][n][e] = -INFINITY;
+          sc[u][n][e] *= ks * qs[n][e & 1];
+          if (!whole && pos[u] + g + (e >> 1) * 8 >= lim[n][e & 1]) sc[u][n][e] = -INFINITY;
         }
     }
-    bool grow = false;
+    bool grow = vmax > vref;
     float mn[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -313,6 +370,8 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
         grow |= x > m[n][e];
       }
     if (__any_sync(0xffffffffu, grow)) {
+      const float vf = kv8_pow2(max(127 + vref - vmax, 0));  // beyond 2^-126: nothing is left of the sums
+      vref = vmax;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float f[2];
@@ -321,6 +380,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
           f[e] = mn[n][e] > m[n][e] ? ex2(m[n][e] - mn[n][e]) : 1.f;  // -inf before the first visible key: 0
           m[n][e] = mn[n][e];
           l[n][e] *= f[e];
+          f[e] *= vf;
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j)
@@ -331,7 +391,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t pf[NQ][2][PP];
-      const float vs = kv8_pow2(st.ve[u]);
+      const float vs = kv8_pow2(max(141 + ve[u] - vref, 0));  // 2^(14 + ve - vref)
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float p[4];
@@ -350,40 +410,44 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
           for (int x = 0; x < PP; ++x) pf[n][e][x] = movmatrix_trans(pl[x]);  // query g, keys 2t + 8 e, 2t + 1 + 8 e
         }
       }
+      uint32_t v[4][VW];
+      const uint8_t* vp = sm.ring[warp][slot][u][1];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) kv8_load_vrow<DH>(v[r], vp + (2 * t + (r & 1) + (r >> 1) * 8) * DH, g);
+      if (pos[u] + kKv8Block > maxlim) {  // weight 0, but what lies there may be no number
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (pos[u] + 2 * t + (r & 1) + (r >> 1) * 8 >= maxlim)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) v[r][i] = 0;
+      }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {  // channels of value bytes 2j and 2j + 1
-        constexpr uint32_t s0 = kv8_sel<FMT>(0, 4), s1 = kv8_sel<FMT>(1, 5), s2 = kv8_sel<FMT>(2, 6), s3 = kv8_sel<FMT>(3, 7);
-        const int w = j >> 1;
-        uint4 f;
-        f.x = kv8_pair<FMT>(st.v[u][0][w], st.v[u][1][w], (j & 1) ? s2 : s0);
-        f.y = kv8_pair<FMT>(st.v[u][0][w], st.v[u][1][w], (j & 1) ? s3 : s1);
-        f.z = kv8_pair<FMT>(st.v[u][2][w], st.v[u][3][w], (j & 1) ? s2 : s0);
-        f.w = kv8_pair<FMT>(st.v[u][2][w], st.v[u][3][w], (j & 1) ? s3 : s1);
+        const uint2 x = kv8_half_pairs<FMT>(v[0][j >> 1], v[1][j >> 1], j & 1), y = kv8_half_pairs<FMT>(v[2][j >> 1], v[3][j >> 1], j & 1);
+        const uint4 f = make_uint4(x.x, x.y, y.x, y.y);
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int p = PP - 1; p >= 0; --p) mma16816(o[j][n], f, pf[n][0][p], pf[n][1][p]);
+          for (int p = PP - 1; p >= 0; --p) mma16816_f16(o[j][n], f, pf[n][0][p], pf[n][1][p]);
       }
     }
   };
 
-  if (steps > 0) {
-    constexpr int PER = 32 / U;  // steps per resolve
-    Stage st[2];
-    resolve(0);
-    load(st[0], 0);
+  {
+    int slot = 0, fill = S - 1;
 #pragma unroll 1
-    for (int it = 0; it < steps; it += 2) {
-      if (it + 1 < steps) load(st[1], it + 1);
-      compute(st[0]);
-      if (it + 1 >= steps) break;
-      if (it + 2 < steps) {
-        if ((it + 2) % PER == 0) resolve(it + 2);
-        load(st[0], it + 2);
-      }
-      compute(st[1]);
+    for (int it = 0; it < steps; ++it) {
+      cp_async_wait<S - 2>();
+      __syncwarp();  // every lane's copies of this step are there, and the slot to fill has been read by all
+      issue(it + S - 1, fill);
+      note(it + S - 1, fill);
+      compute(slot);
+      slot = slot + 1 == S ? 0 : slot + 1;
+      fill = fill + 1 == S ? 0 : fill + 1;
     }
+    cp_async_wait<0>();
   }
+  __syncthreads();  // the ring's memory takes the partial outputs
 
   // ---- join the warps
 #pragma unroll
@@ -391,14 +455,15 @@ __global__ void __launch_bounds__(kKv8Warps * 32) k_kv8_attend(const __grid_cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float x = l[n][e];
+      const float vs = kv8_pow2(vref - 14);
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int qn = n * 8 + 2 * t + e;
       if (g == 0) sm.m[warp][qn] = m[n][e], sm.l[warp][qn] = x;
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        sm.o[warp][qn][kv8_vdim<DH>(2 * j, g)] = o[j][n][e];
-        sm.o[warp][qn][kv8_vdim<DH>(2 * j + 1, g)] = o[j][n][e + 2];
+        sm.o[warp][qn][kv8_vdim<DH>(2 * j, g)] = o[j][n][e] * vs;
+        sm.o[warp][qn][kv8_vdim<DH>(2 * j + 1, g)] = o[j][n][e + 2] * vs;
       }
     }
   __syncthreads();
@@ -488,12 +553,13 @@ template <int DH, int FMT>
 cudaError_t kv8_attend_dh(const Kv8View& c, const Kv8AttnArgs& a, int max_keys, int sm_count, cudaStream_t st) {
   // queries a tile: 8, or 16 where a tile can hold more than 8
   const bool wide = (a.sel_pages ? a.G : (long long)a.max_rows * a.G) > 8;
+  // planes (11 bits each) of the queries and of the weights: fp32 two and two; bf16 and f16 queries fit one; weights one
+  // for bf16 (its own step is 16 times coarser) and two for f16
   if (a.dtype == BLT_T_F32)
-    return wide && DH <= 64 ? kv8_attend_one<DH, FMT, 3, 3, (DH <= 64 ? 2 : 1)>(c, a, max_keys, sm_count, st)
-                            : kv8_attend_one<DH, FMT, 3, 3, 1>(c, a, max_keys, sm_count, st);
+    return wide ? kv8_attend_one<DH, FMT, 2, 2, 2>(c, a, max_keys, sm_count, st) : kv8_attend_one<DH, FMT, 2, 2, 1>(c, a, max_keys, sm_count, st);
   if (a.dtype == BLT_T_BF16)
-    return wide ? kv8_attend_one<DH, FMT, 1, 2, 2>(c, a, max_keys, sm_count, st) : kv8_attend_one<DH, FMT, 1, 2, 1>(c, a, max_keys, sm_count, st);
-  return wide ? kv8_attend_one<DH, FMT, 2, 2, 2>(c, a, max_keys, sm_count, st) : kv8_attend_one<DH, FMT, 2, 2, 1>(c, a, max_keys, sm_count, st);
+    return wide ? kv8_attend_one<DH, FMT, 1, 1, 2>(c, a, max_keys, sm_count, st) : kv8_attend_one<DH, FMT, 1, 1, 1>(c, a, max_keys, sm_count, st);
+  return wide ? kv8_attend_one<DH, FMT, 1, 2, 2>(c, a, max_keys, sm_count, st) : kv8_attend_one<DH, FMT, 1, 2, 1>(c, a, max_keys, sm_count, st);
 }
 
 }  // namespace bltdec

@@ -112,17 +112,18 @@ class Cache:
             out.append(x.transpose(1, 0, 2, 3).reshape(self.H, -1, self.D))
         return out
 
-    def attend(self, s, q, limit, scale, pages=None, mantissa=24, planes=24):
+    def attend(self, s, q, limit, scale, pages=None, mantissa=22, planes=22):
         """q float64 [Hq, D] of one row -> out [Hq, D], lse [Hq], and error bounds of both for a kernel that sums in
-        fp32 with q used to `mantissa` bits and weights to `planes` bits.  pages: list per key/value head, or None.
+        fp32 with q used to `mantissa` bits and weights to `planes` bits (relative errors 2^-mantissa and 2^-planes), both
+        through f16 after a scaling that puts the largest at 2^14 or above, so that f16's least step (2^-24) is 2^-38 of
+        it.  pages: list per key/value head, or None.
 
         A score is a sum of D products taken in fp32 (at most D + 4 roundings, each of at most 2^-23 of the sum of
-        magnitudes: the tensor core may cut instead of round) from a q off by 2^-mantissa of itself; all scores off by
-        d move each weight by a factor exp(+-2 d).  An output is a sum of L weighted values: weights off by 2^-planes,
-        the exponential and its argument's rounding (2^-22 (1 + |score|)), and at most L / 4 + 64 roundings of 2^-23.
-        Weights are taken relative to the largest, so what fp32 flushes (below 2^-126, once where a weight is made and
-        once where partial sums are joined, with the last plane of a split weight) moves an output by at most
-        2^-124 sum |v|: that counts only where every larger weight meets a value of 0."""
+        magnitudes: the tensor core may cut instead of round) from a q off by 2^-mantissa of itself or by half of f16's
+        least step; all scores off by d move each weight by a factor exp(+-2 d).  An output is a sum of L weighted values:
+        weights off by 2^-planes, the exponential and its argument's rounding (2^-22 (1 + |score|)), and at most L / 4 + 64
+        roundings of 2^-23.  Weights times their block's scale are taken relative to 1 times the largest scale: off by
+        half of f16's least step, 2^-39, each times a code of at most top."""
         Hq = len(q)
         G = Hq // self.H
         out, lse = np.zeros((Hq, self.D)), np.full(Hq, -np.inf)
@@ -146,8 +147,10 @@ class Cache:
             out[h] = p @ v
             mag = float((abs(scale) * (np.abs(k) @ np.abs(q[h]))).max())
             d = mag * ((self.D + 4) * 2.0 ** -23 + 2.0 ** -mantissa) + 2.0 ** -22 * (1 + np.abs(z).max())
+            d += 2.0 ** -39 * float(abs(scale) * np.abs(q[h]).max() * np.abs(k).sum(1).max())
+            top = TOP[self.fmt] * 2.0 ** (float(self.v_exp[self.table[s, mine], kv].reshape(-1)[see.reshape(-1, 16).any(1)].max()) - 127)
             n = (len(z) / 4 + 64) * 2.0 ** -23
-            eo[h] = (p @ np.abs(v)) * (2 * d + n + 2.0 ** -planes) + 2.0 ** -124 * np.abs(v).sum(0)
+            eo[h] = (p @ np.abs(v)) * (2 * d + n + 2.0 ** -planes) + 2.0 ** -38 * len(z) * top
             el[h] = d + n + 2.0 ** -22 * (1 + abs(lse[h]))
         return out, lse, eo, el
 
