@@ -582,6 +582,7 @@ int blt_kv8_attend(const blt_kv8_cache* c, const blt_kv8_attention* t, void* str
   a.row_off = t->row_offsets, a.row_limit = t->row_limit;
   a.sel_pages = t->sel_pages, a.sel_count = t->sel_count, a.n_select = t->n_select;
   a.q_vec = !misaligned(t->q, 16) && t->q_row_stride * es % 16 == 0 && t->q_head_stride * es % 16 == 0;
+  a.out_vec = !misaligned(t->out, 16) && t->out_row_stride * es % 16 == 0 && t->out_head_stride * es % 16 == 0;
   const cudaError_t e = kv8_attend_launch(c->format, c->head_dim, v, a, t->max_keys, (cudaStream_t)stream);
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -222,7 +222,7 @@ struct Kv8AttnArgs {
   const int *row_off, *row_limit;
   const int *sel_pages, *sel_count;
   int n_select;
-  int q_vec;  // q rows allow aligned loads of four consecutive channels
+  int q_vec, out_vec;  // rows of q (out) allow 16-byte loads (stores)
 };
 cudaError_t kv8_attend_launch(int fmt, int dh, const Kv8View& c, const Kv8AttnArgs& a, int max_keys, cudaStream_t st);
 

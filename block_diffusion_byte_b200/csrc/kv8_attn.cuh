@@ -528,13 +528,9 @@ cudaError_t kv8_attend_one(const Kv8View& c, const Kv8AttnArgs& a, int max_keys,
   keys = max(keys, 1ll);
   // Split the key axis over a cluster while the CTAs do not fill the GPU and each keeps a step per warp.
   int cl = 1;
-  while (cl < 16 && tiles * c.H * c.batch * cl < sm_count && keys >= (long long)cl * 2 * kKv8Warps * kKv8Block) cl *= 2;
+  while (cl < 8 && tiles * c.H * c.batch * cl < sm_count && keys >= (long long)cl * 2 * kKv8Warps * kKv8Block) cl *= 2;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if (cl > 8) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * cl), (unsigned)c.H, (unsigned)c.batch);
   cfg.blockDim = dim3(kKv8Warps * 32);
@@ -549,8 +545,16 @@ cudaError_t kv8_attend_one(const Kv8View& c, const Kv8AttnArgs& a, int max_keys,
   return cudaLaunchKernelEx(&cfg, kern, c, a, cl);
 }
 
+constexpr int kKv8TileRows = 96;
+template <int DH, int FMT>
+cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t st);
+
 template <int DH, int FMT>
 cudaError_t kv8_attend_dh(const Kv8View& c, const Kv8AttnArgs& a, int max_keys, int sm_count, cudaStream_t st) {
+  // many rows: tiles of 128 queries on tcgen05
+  const long long tiles = ((long long)a.max_rows * a.G + 127) / 128;
+  if (!a.sel_pages && (long long)a.max_rows * a.G >= kKv8TileRows && tiles * c.H * c.batch < INT_MAX)
+    return kv8_tile_dh<DH, FMT>(c, a, tiles, st);
   // queries a tile: 8, or 16 where a tile can hold more than 8
   const bool wide = (a.sel_pages ? a.G : (long long)a.max_rows * a.G) > 8;
   // planes (11 bits each) of the queries and of the weights: fp32 two and two; bf16 and f16 queries fit one; weights one

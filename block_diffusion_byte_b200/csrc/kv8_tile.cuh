@@ -1,0 +1,462 @@
+// Attention over the 8-bit paged KV cache for many query rows (prompts): 128 queries against tiles of keys on the
+// 5th-generation tensor cores.
+//
+// A CTA takes 128 queries -- (row, query head) pairs of one sequence that share a key/value head -- and walks its
+// keys in tiles of N.  Per tile  S = Q K^T  (128 x N, fp32 in tensor memory),  P = exp2(S c - m),  O += P V  with P read
+// from tensor memory, so neither S nor P passes through shared memory.  Three roles:
+//   warps 0-3  a thread a query: S from tensor memory, running maximum and sum, P back into tensor memory;
+//   warps 4-6  codes from global memory, a tile ahead in registers, to f16 operands in shared memory (128-byte
+//              swizzle: K as rows of channels, V as rows of channels too, taken MN-major), a few tiles deep;
+//   warp 7     one thread issues the products.
+// Two CTAs share an SM, so one's products run under the other's exponentials.  Codes are whole in f16 times a power of
+// two, relative to the largest scale of the tile; that scale joins the factor of the exponent's argument (keys) or the
+// weights (values), so no instruction is spent on scales outside the conversion.  O is corrected only when a row's
+// maximum has grown by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
+// Bound by the exponentials (one a weight on the 16-a-clock unit) and by issue slots: the products at DH 64 take half
+// that time.  Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
+#pragma once
+
+#include "kv8.cuh"
+#include "kv8_attn.cuh"
+
+namespace bltdec {
+
+constexpr int kKvtQ = 128;                            // queries a tile (tensor memory lanes)
+constexpr int kKvtThreads = 256;                      // 16 warps of two CTAs leave 128 registers a thread
+constexpr int kKvtLoaders = 96;
+constexpr unsigned long long kKvtWaitNs = 1000000000ull;
+constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
+constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
+
+constexpr int kKvtN = 64;                             // keys a tile
+template <int DH>
+__host__ __device__ constexpr int kvt_slots() { return DH <= 64 ? 4 : 2; }  // tiles of operands in shared memory
+template <int DH>
+__host__ __device__ constexpr int kvt_cols() { return DH <= 64 ? 64 : 128; }  // columns of O (whole swizzle atoms of V)
+
+template <int DH, int QP>
+struct KvtSmem {
+  static constexpr int HALVES = DH > 64 ? 2 : 1;  // swizzle atoms of 64 channels
+  uint8_t q[QP][HALVES][kKvtQ * 128];
+  static constexpr int SLOTS = kvt_slots<DH>();
+  uint8_t k[SLOTS][HALVES][kKvtN * 128];
+  uint8_t v[SLOTS][HALVES][kKvtN * 128];
+  int4 meta[SLOTS];  // a tile's key exponent, value exponent, missing blocks (bits)
+  uint64_t q_full, kv_full[SLOTS], kv_empty[SLOTS], s_full[2], p_full, o_done;
+  uint32_t tmem;
+  int max_lim;
+};
+template <int DH, int QP>
+constexpr size_t kvt_smem() { return sizeof(KvtSmem<DH, QP>) + 1024; }
+
+// ------------------------------------------------------------------------ primitives
+// Shared-memory operand of 128-byte rows with 128-byte swizzle, 8-row groups 1024 bytes apart.  `lead`: bytes between
+// atoms of 64 channels for an MN-major operand (unused for a K-major one).
+__device__ __forceinline__ uint64_t kvt_desc(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// f16 x f16 -> fp32, M 128, N n; A K-major; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t kvt_idesc(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kKvtQ >> 4) << 24);
+}
+__device__ __forceinline__ void kvt_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void kvt_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
+      "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void kvt_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void kvt_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void kvt_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void kvt_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void kvt_ld_wait(float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // the values are read after the wait
+}
+__device__ __forceinline__ void kvt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void kvt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ unsigned long long kvt_now() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool kvt_wait(uint64_t* b, unsigned parity) {
+  if (mbar_try(b, parity)) return true;
+  const unsigned long long t0 = kvt_now();
+  while (!mbar_try(b, parity))
+    if (kvt_now() - t0 > kKvtWaitNs) return false;
+  return true;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// 2^-k as two f16, k >= 0; 0 beyond f16's range.
+__device__ __forceinline__ uint32_t kvt_pow2_f16x2(int k) {
+  const uint32_t h = k <= 14 ? (uint32_t)(15 - k) << 10 : k <= 24 ? 1u << (24 - k) : 0u;
+  return h | h << 16;
+}
+// Chunk c (16 bytes, 8 f16) of a 128-byte row in the 128-byte swizzle.
+__device__ __forceinline__ int kvt_swz(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
+
+// grid: query tiles x sequences x key/value heads, flat, the tile slowest and the last tile (the most keys of a causal
+// prompt) first, so that long CTAs start early.
+template <int DH, int FMT, int QP, int PP>
+__global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 ? 2 : 1)
+    k_kv8_tile(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a, const int n_tiles) {
+  constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH>();
+  constexpr int COL_O = 2 * N;  // tensor memory: two tiles of S (P's planes in place, N / 2 columns each), O
+  extern __shared__ uint8_t kvt_raw[];
+  KvtSmem<DH, QP>& sm = *reinterpret_cast<KvtSmem<DH, QP>*>((reinterpret_cast<uintptr_t>(kvt_raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x % c.H, s = blockIdx.x / c.H % c.batch, tile = n_tiles - 1 - (int)(blockIdx.x / c.H / c.batch);
+  int r0, r1;
+  kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
+  const int qbase = tile * kKvtQ, nq = min((r1 - r0) * a.G - qbase, kKvtQ);
+  if (nq <= 0) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, kKvtQ);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(sm.kv_full + i, kKvtLoaders);
+      mbar_init(sm.kv_empty + i, 1);
+    }
+    mbar_init(sm.s_full, 1);
+    mbar_init(sm.s_full + 1, 1);
+    mbar_init(&sm.p_full, kKvtQ);
+    mbar_init(&sm.o_done, 1);
+    sm.max_lim = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 7) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(256));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  int lim = 0;
+  const int cap = c.max_pages * c.PT;
+  const int qrow = r0 + (qbase + (int)threadIdx.x) / a.G, qhead = kvh * a.G + (qbase + (int)threadIdx.x) % a.G;
+  if (warp < 4 && (int)threadIdx.x < nq) {
+    lim = __ldg(a.row_limit + qrow);
+    if (lim > cap) {
+      if (c.status) set_status(c.status, kErrDevice);
+      lim = cap;
+    }
+    lim = max(lim, 0);
+  }
+  __syncthreads();
+  if (warp < 4) {
+    const int wl = __reduce_max_sync(0xffffffffu, lim);
+    if (lane == 0) atomicMax(&sm.max_lim, wl);
+  }
+  kvt_before();
+  __syncthreads();
+  kvt_after();
+  const uint32_t tmem = sm.tmem;
+  const int max_lim = sm.max_lim, nt = (max_lim + N - 1) / N;
+  bool ok = true;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ a thread a query
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const bool mine = (int)threadIdx.x < nq;
+    // the query scaled so that its largest channel lies in [2^14, 2^15), the sign of the scale with it
+    const long long qat = mine ? (long long)qrow * a.qs + (long long)qhead * a.qhs : 0;
+    float big = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < DH; i += 8) {
+      float x[8] = {};
+      if (mine) kv8_ld8(a.q, a.dtype, qat + i, a.q_vec, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+    }
+    const int ex = max((int)(__float_as_uint(big) >> 23), 15);
+    const float up = a.scale == 0.f ? 0.f : copysignf(kv8_pow2(268 - ex), a.scale);
+    const float qs = a.scale == 0.f ? 1.f : kv8_pow2(ex - 14) * (fabsf(a.scale) * 1.4426950408889634f);
+#pragma unroll 2
+    for (int i = 0; i < DH; i += 8) {
+      float x[8] = {};
+      if (mine) kv8_ld8(a.q, a.dtype, qat + i, a.q_vec, x);
+      uint32_t w[4][QP];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) kv8_planes<QP>(x[2 * e] * up, x[2 * e + 1] * up, w[e]);
+#pragma unroll
+      for (int p = 0; p < QP; ++p)
+        *reinterpret_cast<uint4*>(&sm.q[p][i / 64][kvt_swz(threadIdx.x, i % 64 / 8)]) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    mbar_arrive(&sm.q_full);
+
+    float m = -INFINITY, l = 0.f;
+    int vrun = kKv8LowExp;
+    for (int j = 0; j < nt; ++j) {
+      const int slot = j % SLOTS;
+      if (!kvt_wait(sm.s_full + (j & 1), (j >> 1) & 1) || !kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) {  // products, meta
+        ok = false;
+        break;
+      }
+      kvt_after();
+      const uint32_t sp = lane_base + (j & 1) * N;
+      float v[N / 32][32];
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
+      const int4 meta = sm.meta[slot];
+      const int pos0 = j * N;
+      const float ks = kv8_pow2(meta.x) * qs;
+      const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim) && meta.z == 0;
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i) kvt_ld_wait(v[i]);
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (pos0 + i >= lim || (meta.z >> (i / kKv8Block) & 1)) v[i / 32][i % 32] = -INFINITY;
+      }
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < N; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], v[i / 32][i % 32]);
+      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      mx = mx == -INFINITY ? mx : mx * ks;
+      // correction: a maximum that has grown too far, or louder values
+      float f = 1.f;
+      if (mx > m + kKvtGrow || (m == -INFINITY && mx > m)) {
+        f = ex2(m - mx);
+        m = mx;
+      }
+      const int vnew = max(vrun, meta.y);
+      l *= f;
+      f *= kv8_pow2(max(127 + vrun - vnew, 0));
+      vrun = vnew;
+      if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+        if (!kvt_wait(&sm.o_done, (j - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        kvt_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          float x[32];
+          kvt_ld32(lane_base + COL_O + c0, x);
+          kvt_ld_wait(x);
+          uint32_t w[2][16];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i >> 4][i & 15] = __float_as_uint(x[i] * f);
+          kvt_st16(lane_base + COL_O + c0, w[0]);
+          kvt_st16(lane_base + COL_O + c0 + 16, w[1]);
+        }
+      }
+      // weights, times 2^(kKvtShift + value exponent below the reference)
+      const int shift = max(kKvtShift + meta.y - vrun, -100);
+      const float off = (float)shift - (m == -INFINITY ? 0.f : m);
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < N / 32; ++i) {
+        uint32_t w[PP][16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float p0 = ex2(fmaf(v[i][e], ks, off)), p1 = ex2(fmaf(v[i][e + 1], ks, off));
+          s0 += p0;
+          s1 += p1;
+          uint32_t pl[PP];
+          kv8_planes<PP>(p0, p1, pl);
+#pragma unroll
+          for (int p = 0; p < PP; ++p) w[p][e >> 1] = pl[p];
+        }
+#pragma unroll
+        for (int p = 0; p < PP; ++p) kvt_st16(sp + p * (N / 2) + i * 16, w[p]);
+      }
+      l += (s0 + s1) * kv8_pow2(127 - shift);
+      kvt_st_wait();
+      kvt_before();
+      mbar_arrive(&sm.p_full);
+    }
+    // ---- out = O / l
+    if (nt > 0 && ok && !kvt_wait(&sm.o_done, (nt - 1) & 1)) ok = false;
+    kvt_after();
+    if (ok) {
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // nothing visible: 0; NaN stays
+      const float fin = inv * kv8_pow2(vrun - kKvtShift);
+      const long long at = (long long)qrow * a.os + (long long)qhead * a.ohs;
+#pragma unroll
+      for (int c0 = 0; c0 < DH; c0 += 32) {
+        float v[32];
+        if (nt > 0) {
+          kvt_ld32(lane_base + COL_O + c0, v);
+          kvt_ld_wait(v);
+        }
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : v[i + e] * fin;
+            kv8_st8(a.out, a.dtype, at + c0 + i, a.out_vec, x);
+          }
+        }
+      }
+      if (mine && a.lse) a.lse[(size_t)qrow * a.Hq + qhead] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+  } else if (warp < 7) {
+    // ------------------------------------------------------------------ codes to operands
+    constexpr int CPR = DH / 16;                                   // 16-byte pieces of a row
+    constexpr int PC = (N * CPR + kKvtLoaders - 1) / kKvtLoaders;  // pieces of K (and of V) a thread has in a tile, at most
+    const int pt = threadIdx.x - 128;
+    // lane b < NB: page of the tile's block b
+    auto page_of = [&](int j) {
+      const int blk = j * NB + lane;
+      if (j >= nt || lane >= NB || blk * kKv8Block >= max_lim) return -1;
+      return kv8_page(c, s, kv8_div_tpp(c, blk));
+    };
+    uint4 kc[PC], vc[PC];
+    int page = page_of(0), ke = 0, ve = 0;
+    auto load = [&](int j) {
+      const int blk = j * NB + lane, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
+      long long base = -1;  // lane b: block b's codes
+      ke = ve = -1;
+      if (page >= 0) {
+        base = (long long)page * c.page_stride + ((long long)kvh * c.PT + sub * kKv8Block) * DH;
+        const size_t e = (size_t)page * c.exp_stride + kvh * c.tpp + sub;
+        ke = __ldg(c.ke + e);
+        ve = __ldg(c.ve + e);
+      }
+#pragma unroll
+      for (int i = 0; i < PC; ++i) {
+        const int pc = i * kKvtLoaders + pt, key = pc / CPR;
+        const long long from = __shfl_sync(0xffffffffu, base, key / kKv8Block & (NB - 1));
+        kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0 && key < N) {
+          const long long at = from + pc % (kKv8Block * CPR) * 16;
+          kc[i] = __ldg(reinterpret_cast<const uint4*>(c.k + at));
+          if (j * N + key < max_lim) vc[i] = __ldg(reinterpret_cast<const uint4*>(c.v + at));  // behind it may be no numbers
+        }
+      }
+    };
+    if (nt > 0) load(0);
+    int next = page_of(1);
+    for (int j = 0; j < nt; ++j) {
+      const int slot = j % SLOTS;
+      if (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const int kref = max(__reduce_max_sync(0xffffffffu, ke), kKv8LowExp), vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
+      const unsigned held = __ballot_sync(0xffffffffu, ke >= 0);
+      // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
+      const int nb = min((max_lim - j * N + kKv8Block - 1) / kKv8Block, NB);
+      if (pt == 0) sm.meta[slot] = make_int4(kref, vref, (int)(~held & ((1u << nb) - 1)), 0);
+      const uint32_t fk = kvt_pow2_f16x2(kref - ke), fv = kvt_pow2_f16x2(vref - ve);  // lane b: block b's factors
+#pragma unroll
+      for (int i = 0; i < PC; ++i) {
+        const int pc = i * kKvtLoaders + pt, key = pc / CPR, ch = pc % CPR * 16, b = key / kKv8Block & (NB - 1);
+        const uint32_t f[2] = {__shfl_sync(0xffffffffu, fk, b), __shfl_sync(0xffffffffu, fv, b)};
+        if (key >= N) continue;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint4 w = kv ? vc[i] : kc[i];
+          uint8_t* dst = kv ? sm.v[slot][ch / 64] : sm.k[slot][ch / 64];
+          const uint2 x0 = kv8_half4<FMT>(w.x), x1 = kv8_half4<FMT>(w.y), x2 = kv8_half4<FMT>(w.z), x3 = kv8_half4<FMT>(w.w);
+          *reinterpret_cast<uint4*>(dst + kvt_swz(key, ch % 64 / 8)) =
+              make_uint4(mul_f16x2(x0.x, f[kv]), mul_f16x2(x0.y, f[kv]), mul_f16x2(x1.x, f[kv]), mul_f16x2(x1.y, f[kv]));
+          *reinterpret_cast<uint4*>(dst + kvt_swz(key, ch % 64 / 8 + 1)) =
+              make_uint4(mul_f16x2(x2.x, f[kv]), mul_f16x2(x2.y, f[kv]), mul_f16x2(x3.x, f[kv]), mul_f16x2(x3.y, f[kv]));
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      mbar_arrive(sm.kv_full + slot);
+      page = next;
+      if (j + 1 < nt) load(j + 1);
+      next = page_of(j + 2);
+    }
+  } else if (lane == 0 && nt > 0) {
+    // ------------------------------------------------------------------ products
+    constexpr uint32_t is = kvt_idesc(N, false), io = kvt_idesc(NV, true);
+    auto scores = [&](int j) {
+      const int slot = j % SLOTS;
+      if (!kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) return false;
+      kvt_after();
+#pragma unroll
+      for (int p = 0; p < QP; ++p)
+#pragma unroll
+        for (int k0 = 0; k0 < DH; k0 += 16)  // 16 channels: 32 bytes inside the swizzle atom
+          kvt_mma_ss(tmem + (j & 1) * N, kvt_desc(smem_u32(sm.q[p][k0 / 64]), 16) + (k0 % 64) / 8,
+                     kvt_desc(smem_u32(sm.k[slot][k0 / 64]), 16) + (k0 % 64) / 8, is, p > 0 || k0 > 0);
+      kvt_commit(sm.s_full + (j & 1));
+      return true;
+    };
+    ok = kvt_wait(&sm.q_full, 0) && scores(0);
+    for (int j = 0; ok && j < nt; ++j) {
+      // the next tile's scores run under this tile's weights; their columns held P of the tile before
+      if ((j > 0 && !kvt_wait(&sm.o_done, (j - 1) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(&sm.p_full, j & 1)) {
+        ok = false;
+        break;
+      }
+      kvt_after();
+      const int slot = j % SLOTS;
+#pragma unroll
+      for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+        for (int k0 = 0; k0 < N; k0 += 16)  // 16 keys: two 8-row groups of V
+          kvt_mma_ts(tmem + COL_O, tmem + (j & 1) * N + p * (N / 2) + k0 / 2, kvt_desc(smem_u32(sm.v[slot][0]), N * 128) + k0 * 8, io,
+                     j > 0 || p < PP - 1 || k0 > 0);
+      kvt_commit(&sm.o_done);
+      kvt_commit(sm.kv_empty + slot);
+    }
+    if (ok) ok = kvt_wait(&sm.o_done, (nt - 1) & 1);  // nothing is in flight when the memory goes
+  }
+  kvt_before();
+  const bool all_ok = __syncthreads_and(ok) != 0;
+  if (warp == 7) {
+    kvt_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256));
+  }
+  if (!all_ok && threadIdx.x == 0 && c.status) set_status(c.status, kErrDevice);
+}
+
+template <int DH, int FMT, int QP, int PP>
+cudaError_t kv8_tile_one(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t stream) {
+  auto kern = k_kv8_tile<DH, FMT, QP, PP>;
+  constexpr int smem = (int)kvt_smem<DH, QP>();
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(tiles * c.H * c.batch), kKvtThreads, smem, stream>>>(c, a, (int)tiles);
+  return cudaSuccess;
+}
+
+template <int DH, int FMT>
+cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t st) {
+  if (a.dtype == BLT_T_F32) return kv8_tile_one<DH, FMT, 2, 2>(c, a, tiles, st);
+  if (a.dtype == BLT_T_BF16) return kv8_tile_one<DH, FMT, 1, 1>(c, a, tiles, st);
+  return kv8_tile_one<DH, FMT, 1, 2>(c, a, tiles, st);
+}
+
+}  // namespace bltdec

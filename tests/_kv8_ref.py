@@ -122,8 +122,8 @@ class Cache:
         magnitudes: the tensor core may cut instead of round) from a q off by 2^-mantissa of itself or by half of f16's
         least step; all scores off by d move each weight by a factor exp(+-2 d).  An output is a sum of L weighted values:
         weights off by 2^-planes, the exponential and its argument's rounding (2^-22 (1 + |score|)), and at most L / 4 + 64
-        roundings of 2^-23.  Weights times their block's scale are taken relative to 1 times the largest scale: off by
-        half of f16's least step, 2^-39, each times a code of at most top."""
+        roundings of 2^-23.  Weights times their block's scale are taken relative to 1 times the largest scale and 2^8 at
+        least: off by half of f16's least step, 2^-33, each times a code of at most top."""
         Hq = len(q)
         G = Hq // self.H
         out, lse = np.zeros((Hq, self.D)), np.full(Hq, -np.inf)
@@ -150,7 +150,7 @@ class Cache:
             d += 2.0 ** -39 * float(abs(scale) * np.abs(q[h]).max() * np.abs(k).sum(1).max())
             top = TOP[self.fmt] * 2.0 ** (float(self.v_exp[self.table[s, mine], kv].reshape(-1)[see.reshape(-1, 16).any(1)].max()) - 127)
             n = (len(z) / 4 + 64) * 2.0 ** -23
-            eo[h] = (p @ np.abs(v)) * (2 * d + n + 2.0 ** -planes) + 2.0 ** -38 * len(z) * top
+            eo[h] = (p @ np.abs(v)) * (2 * d + n + 2.0 ** -planes) + 2.0 ** -33 * len(z) * top
             el[h] = d + n + 2.0 ** -22 * (1 + abs(lse[h]))
         return out, lse, eo, el
 
