@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
                                                                 const int CL) {
   constexpr int U = kv8_units<DH>(), S = kKv8Stages;
   constexpr int KW = DH / 16, VW = DH / 32, MT = DH / 16;
+  constexpr int DT = QP == 2 ? BLT_T_F32 : PP == 1 ? BLT_T_BF16 : BLT_T_F16;  // a.dtype
   extern __shared__ float4 kv8_smem4[];
   Kv8Smem<DH, NQ>& sm = *reinterpret_cast<Kv8Smem<DH, NQ>*>(kv8_smem4);
   const int tile = blockIdx.x / CL, rank = blockIdx.x % CL, kvh = blockIdx.y, s = blockIdx.z;
@@ -281,18 +282,20 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     const int qn = n * 8 + g;
     const long long base = qn < nq ? (long long)row_of(qn) * a.qs + (long long)head_of(qn) * a.qhs : 0;
     float x[KW][4];
+#pragma unroll
+    for (int i = 0; i < KW; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    if (qn < nq && a.q_vec) {
+#pragma unroll
+      for (int i = 0; i < KW; ++i) kv8_ld4(a.q, DT, base + kv8_kdim<DH>(i, t), true, x[i]);
+    } else if (qn < nq) {
+#pragma unroll
+      for (int i = 0; i < KW; ++i) kv8_ld4(a.q, DT, base + kv8_kdim<DH>(i, t), false, x[i]);
+    }
     float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < KW; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
-      if (qn < nq) {
-        const long long at = base + kv8_kdim<DH>(i, t);
-        kv8_ld4(a.q, a.dtype, at, a.q_vec, x[i]);
-      }
+    for (int i = 0; i < KW; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(x[i][j]));
-    }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
     const int ex = max((int)(__float_as_uint(big) >> 23), 15);
@@ -471,10 +474,10 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   auto finish = [&](int qn, int d, float4 v, float M, float L) {
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // nothing visible: 0; NaN stays
     const long long at = (long long)row_of(qn) * a.os + (long long)head_of(qn) * a.ohs + d;
-    kv8_st(a.out, a.dtype, at, v.x * inv);
-    kv8_st(a.out, a.dtype, at + 1, v.y * inv);
-    kv8_st(a.out, a.dtype, at + 2, v.z * inv);
-    kv8_st(a.out, a.dtype, at + 3, v.w * inv);
+    kv8_st(a.out, DT, at, v.x * inv);
+    kv8_st(a.out, DT, at + 1, v.y * inv);
+    kv8_st(a.out, DT, at + 2, v.z * inv);
+    kv8_st(a.out, DT, at + 3, v.w * inv);
     if (d == 0 && a.lse) a.lse[(size_t)row_of(qn) * a.Hq + head_of(qn)] = L == 0.f ? -INFINITY : (M + log2f(L)) * ln2;
   };
   for (int i = threadIdx.x; i < nq * (DH / 4); i += kKv8Warps * 32) {

@@ -5,8 +5,9 @@
 // keys in tiles of N.  Per tile  S = Q K^T  (128 x N, fp32 in tensor memory),  P = exp2(S c - m),  O += P V  with P read
 // from tensor memory, so neither S nor P passes through shared memory.  Three roles:
 //   warps 0-3  a thread a query: S from tensor memory, running maximum and sum, P back into tensor memory;
-//   warps 4-6  codes from global memory, a tile ahead in registers, to f16 operands in shared memory (128-byte
-//              swizzle: K as rows of channels, V as rows of channels too, taken MN-major), a few tiles deep;
+//   warps 4-6  codes to f16 operands in shared memory (128-byte swizzle: K as rows of channels, V as rows of channels
+//              too, taken MN-major), a few tiles deep.  The codes of a block of 16 positions are one bulk copy into the
+//              place of the operand, converted there;
 //   warp 7     one thread issues the products.
 // Two CTAs share an SM, so one's products run under the other's exponentials.  Codes are whole in f16 times a power of
 // two, relative to the largest scale of the tile; that scale joins the factor of the exponent's argument (keys) or the
@@ -23,14 +24,16 @@ namespace bltdec {
 
 constexpr int kKvtQ = 128;                            // queries a tile (tensor memory lanes)
 constexpr int kKvtThreads = 256;                      // 16 warps of two CTAs leave 128 registers a thread
-constexpr int kKvtLoaders = 96;
-constexpr unsigned long long kKvtWaitNs = 1000000000ull;
+constexpr int kKvtLoaders = 3;                        // warps that convert, a tile each in turn
+constexpr long long kKvtWaitClocks = 2000000000ll;    // about a second
 constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
 
 constexpr int kKvtN = 64;                             // keys a tile
 template <int DH>
 __host__ __device__ constexpr int kvt_slots() { return DH <= 64 ? 4 : 2; }  // tiles of operands in shared memory
+template <int DH>
+__host__ __device__ constexpr int kvt_bufs() { return DH <= 64 ? 3 : 2; }  // tiles of S in tensor memory (256 columns a CTA)
 template <int DH>
 __host__ __device__ constexpr int kvt_cols() { return DH <= 64 ? 64 : 128; }  // columns of O (whole swizzle atoms of V)
 
@@ -42,7 +45,7 @@ struct KvtSmem {
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
   int4 meta[SLOTS];  // a tile's key exponent, value exponent, missing blocks (bits)
-  uint64_t q_full, kv_full[SLOTS], kv_empty[SLOTS], s_full[2], p_full, o_done;
+  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH>()], p_full, o_done[kvt_bufs<DH>()];
   uint32_t tmem;
   int max_lim;
 };
@@ -76,6 +79,11 @@ __device__ __forceinline__ void kvt_mma_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
+__device__ __forceinline__ bool kvt_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void kvt_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -106,17 +114,17 @@ __device__ __forceinline__ void kvt_st16(uint32_t taddr, const uint32_t (&r)[16]
       : "memory");
 }
 __device__ __forceinline__ void kvt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ unsigned long long kvt_now() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
+// A whole warp waits for phase `parity` of a barrier; false for all its lanes once the time is up.  (The SM's clock, not
+// the global timer, whose reading takes as long as a product.)
 __device__ __forceinline__ bool kvt_wait(uint64_t* b, unsigned parity) {
-  if (mbar_try(b, parity)) return true;
-  const unsigned long long t0 = kvt_now();
-  while (!mbar_try(b, parity))
-    if (kvt_now() - t0 > kKvtWaitNs) return false;
-  return true;
+  bool done = mbar_try(b, parity);
+  if (__all_sync(0xffffffffu, done)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    done = done || mbar_try(b, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (__any_sync(0xffffffffu, clock64() - t0 > kKvtWaitClocks)) return false;
+  }
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -136,11 +144,12 @@ __device__ __forceinline__ int kvt_swz(int row, int c) { return row * 128 + ((c 
 template <int DH, int FMT, int QP, int PP>
 __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 ? 2 : 1)
     k_kv8_tile(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a, const int n_tiles) {
-  constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH>();
-  constexpr int COL_O = 2 * N;  // tensor memory: two tiles of S (P's planes in place, N / 2 columns each), O
+  constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH>(), BUFS = kvt_bufs<DH>();
+  constexpr int COL_O = BUFS * N;  // tensor memory: tiles of S (P's planes in place, N / 2 columns each), O
+  constexpr int DT = QP == 2 ? BLT_T_F32 : PP == 1 ? BLT_T_BF16 : BLT_T_F16;  // a.dtype
   extern __shared__ uint8_t kvt_raw[];
   KvtSmem<DH, QP>& sm = *reinterpret_cast<KvtSmem<DH, QP>*>((reinterpret_cast<uintptr_t>(kvt_raw) + 1023) & ~(uintptr_t)1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int kvh = blockIdx.x % c.H, s = blockIdx.x / c.H % c.batch, tile = n_tiles - 1 - (int)(blockIdx.x / c.H / c.batch);
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
@@ -150,13 +159,15 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, kKvtQ);
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(sm.kv_full + i, kKvtLoaders);
+      mbar_init(sm.raw_full + i, 1);
+      mbar_init(sm.kv_full + i, 32);
       mbar_init(sm.kv_empty + i, 1);
     }
-    mbar_init(sm.s_full, 1);
-    mbar_init(sm.s_full + 1, 1);
+    for (int i = 0; i < BUFS; ++i) {
+      mbar_init(sm.s_full + i, 1);
+      mbar_init(sm.o_done + i, 1);
+    }
     mbar_init(&sm.p_full, kKvtQ);
-    mbar_init(&sm.o_done, 1);
     sm.max_lim = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -193,27 +204,45 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     const bool mine = (int)threadIdx.x < nq;
     // the query scaled so that its largest channel lies in [2^14, 2^15), the sign of the scale with it
     const long long qat = mine ? (long long)qrow * a.qs + (long long)qhead * a.qhs : 0;
+    constexpr int QC = DH <= 64 ? DH : 32;  // channels in registers at once (all loads of a row in flight where they fit)
+    float x[QC];
     float big = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < DH; i += 8) {
-      float x[8] = {};
-      if (mine) kv8_ld8(a.q, a.dtype, qat + i, a.q_vec, x);
+    auto fetch = [&](int c0) {
+      if (a.q_vec) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+        for (int i = 0; i < QC; i += 8) {
+          float y[8] = {};
+          if (mine) kv8_ld8(a.q, DT, qat + c0 + i, true, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i + e] = y[e];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) x[i] = mine ? kv8_ld(a.q, DT, qat + c0 + i) : 0.f;
+      }
+    };
+#pragma unroll
+    for (int c0 = 0; c0 < DH; c0 += QC) {
+      fetch(c0);
+#pragma unroll
+      for (int i = 0; i < QC; ++i) big = fmaxf(big, fabsf(x[i]));
     }
     const int ex = max((int)(__float_as_uint(big) >> 23), 15);
     const float up = a.scale == 0.f ? 0.f : copysignf(kv8_pow2(268 - ex), a.scale);
     const float qs = a.scale == 0.f ? 1.f : kv8_pow2(ex - 14) * (fabsf(a.scale) * 1.4426950408889634f);
-#pragma unroll 2
-    for (int i = 0; i < DH; i += 8) {
-      float x[8] = {};
-      if (mine) kv8_ld8(a.q, a.dtype, qat + i, a.q_vec, x);
-      uint32_t w[4][QP];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) kv8_planes<QP>(x[2 * e] * up, x[2 * e + 1] * up, w[e]);
+    for (int c0 = 0; c0 < DH; c0 += QC) {
+      if (QC < DH) fetch(c0);
 #pragma unroll
-      for (int p = 0; p < QP; ++p)
-        *reinterpret_cast<uint4*>(&sm.q[p][i / 64][kvt_swz(threadIdx.x, i % 64 / 8)]) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+      for (int i = 0; i < QC; i += 8) {
+        uint32_t w[4][QP];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kv8_planes<QP>(x[i + 2 * e] * up, x[i + 2 * e + 1] * up, w[e]);
+#pragma unroll
+        for (int p = 0; p < QP; ++p)
+          *reinterpret_cast<uint4*>(&sm.q[p][(c0 + i) / 64][kvt_swz(threadIdx.x, (c0 + i) % 64 / 8)]) =
+              make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+      }
     }
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     mbar_arrive(&sm.q_full);
@@ -222,12 +251,12 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     int vrun = kKv8LowExp;
     for (int j = 0; j < nt; ++j) {
       const int slot = j % SLOTS;
-      if (!kvt_wait(sm.s_full + (j & 1), (j >> 1) & 1) || !kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) {  // products, meta
+      if (!kvt_wait(sm.s_full + j % BUFS, (j / BUFS) & 1) || !kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) {  // products, meta
         ok = false;
         break;
       }
       kvt_after();
-      const uint32_t sp = lane_base + (j & 1) * N;
+      const uint32_t sp = lane_base + j % BUFS * N;
       float v[N / 32][32];
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
@@ -258,7 +287,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       f *= kv8_pow2(max(127 + vrun - vnew, 0));
       vrun = vnew;
       if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-        if (!kvt_wait(&sm.o_done, (j - 1) & 1)) {
+        if (!kvt_wait(sm.o_done + (j - 1) % BUFS, ((j - 1) / BUFS) & 1)) {
           ok = false;
           break;
         }
@@ -301,7 +330,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       mbar_arrive(&sm.p_full);
     }
     // ---- out = O / l
-    if (nt > 0 && ok && !kvt_wait(&sm.o_done, (nt - 1) & 1)) ok = false;
+    if (nt > 0 && ok && !kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
     kvt_after();
     if (ok) {
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // nothing visible: 0; NaN stays
@@ -320,7 +349,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : v[i + e] * fin;
-            kv8_st8(a.out, a.dtype, at + c0 + i, a.out_vec, x);
+            kv8_st8(a.out, DT, at + c0 + i, a.out_vec, x);
           }
         }
       }
@@ -328,110 +357,141 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     }
   } else if (warp < 7) {
     // ------------------------------------------------------------------ codes to operands
-    constexpr int CPR = DH / 16;                                   // 16-byte pieces of a row
-    constexpr int PC = (N * CPR + kKvtLoaders - 1) / kKvtLoaders;  // pieces of K (and of V) a thread has in a tile, at most
-    const int pt = threadIdx.x - 128;
-    // lane b < NB: page of the tile's block b
-    auto page_of = [&](int j) {
+    // A warp takes whole tiles, every third one: its copies are in flight while the others convert.
+    constexpr int CPR = DH / 16;         // 16-byte pieces of a row
+    constexpr int PC = N * CPR / 32;     // pieces of K (and of V) a lane has in a tile
+    const int first = warp - 4;
+    // lane b < NB: the table's entry for the tile's block b, INT_MIN if it has none.  The entry is looked at when the
+    // codes are asked for, a tile later: looking at it here would wait for it.
+    auto entry_of = [&](int j) {
       const int blk = j * NB + lane;
-      if (j >= nt || lane >= NB || blk * kKv8Block >= max_lim) return -1;
-      return kv8_page(c, s, kv8_div_tpp(c, blk));
+      if (j >= nt || lane >= NB || blk * kKv8Block >= max_lim) return INT_MIN;
+      return __ldg(c.table + (size_t)s * c.max_pages + kv8_div_tpp(c, blk));
     };
-    uint4 kc[PC], vc[PC];
-    int page = page_of(0), ke = 0, ve = 0;
-    auto load = [&](int j) {
-      const int blk = j * NB + lane, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
-      long long base = -1;  // lane b: block b's codes
-      ke = ve = -1;
-      if (page >= 0) {
-        base = (long long)page * c.page_stride + ((long long)kvh * c.PT + sub * kKv8Block) * DH;
-        const size_t e = (size_t)page * c.exp_stride + kvh * c.tpp + sub;
+    // Where block b's codes are put: in the operand's own place, such that a part (all keys, or with two swizzle atoms
+    // the first and the second 32) is read whole before anything is written over it.
+    constexpr int PARTS = KvtSmem<DH, QP>::HALVES, PCH = PC / PARTS, BP = NB / PARTS;
+    auto raw_of = [&](uint8_t (*dst)[N * 128], int b) {
+      return PARTS == 1 ? dst[0] + b * kKv8Block * DH : dst[b / BP] + N * 64 + b % BP * kKv8Block * DH;
+    };
+    // The tile's codes as f16 times lane b's factor for block b.  Blocks that are not `held`, and rows from `rows` on
+    // (they may be no numbers), become 0.
+    auto convert = [&](uint8_t (*dst)[N * 128], uint32_t fac, unsigned held, int rows) {
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        uint4 w[PCH];
+        const uint4* raw = reinterpret_cast<const uint4*>(raw_of(dst, h * BP));
+#pragma unroll
+        for (int i = 0; i < PCH; ++i) w[i] = raw[i * 32 + lane];
+        __syncwarp();
+        if (held != (1u << NB) - 1 || rows < N) {
+#pragma unroll
+          for (int i = 0; i < PCH; ++i) {
+            const int key = h * (N / PARTS) + (i * 32 + lane) / CPR;
+            if (!(held >> (key / kKv8Block) & 1) || key >= rows) w[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PCH; ++i) {
+          const int pc = i * 32 + lane, key = h * (N / PARTS) + pc / CPR, ch = pc % CPR * 16;
+          const uint32_t f = __shfl_sync(0xffffffffu, fac, key / kKv8Block);
+          const uint2 x0 = kv8_half4<FMT>(w[i].x), x1 = kv8_half4<FMT>(w[i].y), x2 = kv8_half4<FMT>(w[i].z), x3 = kv8_half4<FMT>(w[i].w);
+          uint8_t* d = dst[ch / 64];
+          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8)) =
+              make_uint4(mul_f16x2(x0.x, f), mul_f16x2(x0.y, f), mul_f16x2(x1.x, f), mul_f16x2(x1.y, f));
+          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8 + 1)) =
+              make_uint4(mul_f16x2(x2.x, f), mul_f16x2(x2.y, f), mul_f16x2(x3.x, f), mul_f16x2(x3.y, f));
+        }
+        if (PARTS > 1) __syncwarp();
+      }
+    };
+    int entry = entry_of(first);
+    for (int j = first; j < nt; j += kKvtLoaders) {
+      const int slot = j % SLOTS;
+      // The slot's last tile is done with.  This warp's last wait was for tile j - 3 - SLOTS; where the slot has had
+      // another tile since (fewer than four slots), that one first: a barrier tells only two phases apart.
+      if ((SLOTS <= kKvtLoaders && j >= 2 * SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS) & 1)) ||
+          (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      const bool there = (unsigned)entry < (unsigned)c.n_pages;
+      if (!there && entry != INT_MIN && c.status) set_status(c.status, kErrDevice);
+      const unsigned held = __ballot_sync(0xffffffffu, there);
+      if (lane == 0) mbar_expect_tx(sm.raw_full + slot, __popc(held) * 2 * kKv8Block * DH);
+      __syncwarp();
+      int ke = -1, ve = -1;
+      if (there) {
+        const int blk = j * NB + lane, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
+        const size_t at = (size_t)entry * c.page_stride + ((size_t)kvh * c.PT + sub * kKv8Block) * DH;
+        bulk_g2s(raw_of(sm.k[slot], lane), c.k + at, kKv8Block * DH, sm.raw_full + slot);
+        bulk_g2s(raw_of(sm.v[slot], lane), c.v + at, kKv8Block * DH, sm.raw_full + slot);
+        const size_t e = (size_t)entry * c.exp_stride + kvh * c.tpp + sub;
         ke = __ldg(c.ke + e);
         ve = __ldg(c.ve + e);
       }
-#pragma unroll
-      for (int i = 0; i < PC; ++i) {
-        const int pc = i * kKvtLoaders + pt, key = pc / CPR;
-        const long long from = __shfl_sync(0xffffffffu, base, key / kKv8Block & (NB - 1));
-        kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-        if (from >= 0 && key < N) {
-          const long long at = from + pc % (kKv8Block * CPR) * 16;
-          kc[i] = __ldg(reinterpret_cast<const uint4*>(c.k + at));
-          if (j * N + key < max_lim) vc[i] = __ldg(reinterpret_cast<const uint4*>(c.v + at));  // behind it may be no numbers
-        }
-      }
-    };
-    if (nt > 0) load(0);
-    int next = page_of(1);
-    for (int j = 0; j < nt; ++j) {
-      const int slot = j % SLOTS;
-      if (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1)) {
+      entry = entry_of(j + kKvtLoaders);
+      if (!kvt_wait(sm.raw_full + slot, (j / SLOTS) & 1)) {
         ok = false;
         break;
       }
       const int kref = max(__reduce_max_sync(0xffffffffu, ke), kKv8LowExp), vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
-      const unsigned held = __ballot_sync(0xffffffffu, ke >= 0);
+      const int rows = min(max_lim - j * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
       // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
-      const int nb = min((max_lim - j * N + kKv8Block - 1) / kKv8Block, NB);
-      if (pt == 0) sm.meta[slot] = make_int4(kref, vref, (int)(~held & ((1u << nb) - 1)), 0);
-      const uint32_t fk = kvt_pow2_f16x2(kref - ke), fv = kvt_pow2_f16x2(vref - ve);  // lane b: block b's factors
-#pragma unroll
-      for (int i = 0; i < PC; ++i) {
-        const int pc = i * kKvtLoaders + pt, key = pc / CPR, ch = pc % CPR * 16, b = key / kKv8Block & (NB - 1);
-        const uint32_t f[2] = {__shfl_sync(0xffffffffu, fk, b), __shfl_sync(0xffffffffu, fv, b)};
-        if (key >= N) continue;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint4 w = kv ? vc[i] : kc[i];
-          uint8_t* dst = kv ? sm.v[slot][ch / 64] : sm.k[slot][ch / 64];
-          const uint2 x0 = kv8_half4<FMT>(w.x), x1 = kv8_half4<FMT>(w.y), x2 = kv8_half4<FMT>(w.z), x3 = kv8_half4<FMT>(w.w);
-          *reinterpret_cast<uint4*>(dst + kvt_swz(key, ch % 64 / 8)) =
-              make_uint4(mul_f16x2(x0.x, f[kv]), mul_f16x2(x0.y, f[kv]), mul_f16x2(x1.x, f[kv]), mul_f16x2(x1.y, f[kv]));
-          *reinterpret_cast<uint4*>(dst + kvt_swz(key, ch % 64 / 8 + 1)) =
-              make_uint4(mul_f16x2(x2.x, f[kv]), mul_f16x2(x2.y, f[kv]), mul_f16x2(x3.x, f[kv]), mul_f16x2(x3.y, f[kv]));
-        }
-      }
+      if (lane == 0) sm.meta[slot] = make_int4(kref, vref, (int)(~held & ((1u << nb) - 1)), 0);
+      convert(sm.k[slot], kvt_pow2_f16x2(kref - ke), held, N);
+      convert(sm.v[slot], kvt_pow2_f16x2(vref - ve), held, rows);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(sm.kv_full + slot);
-      page = next;
-      if (j + 1 < nt) load(j + 1);
-      next = page_of(j + 2);
     }
-  } else if (lane == 0 && nt > 0) {
-    // ------------------------------------------------------------------ products
+  } else if (nt > 0) {
+    // ------------------------------------------------------------------ products: the warp together, one lane issuing
     constexpr uint32_t is = kvt_idesc(N, false), io = kvt_idesc(NV, true);
+    constexpr uint32_t QSTEP = kKvtQ * 128 / 16, KSTEP = N * 128 / 16, KSLOT = KvtSmem<DH, QP>::HALVES * KSTEP;  // in descriptors' units
+    const bool lead = kvt_elect();
+    const uint64_t qd = kvt_desc(smem_u32(sm.q), 16), kd = kvt_desc(smem_u32(sm.k), 16), vd = kvt_desc(smem_u32(sm.v), N * 128);
     auto scores = [&](int j) {
-      const int slot = j % SLOTS;
+      const int slot = j % SLOTS, buf = j % BUFS;
       if (!kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) return false;
       kvt_after();
+      if (lead) {
+        const uint64_t kj = kd + (uint32_t)slot * KSLOT;
+        const uint32_t d = tmem + buf * N;
 #pragma unroll
-      for (int p = 0; p < QP; ++p)
+        for (int p = 0; p < QP; ++p)
 #pragma unroll
-        for (int k0 = 0; k0 < DH; k0 += 16)  // 16 channels: 32 bytes inside the swizzle atom
-          kvt_mma_ss(tmem + (j & 1) * N, kvt_desc(smem_u32(sm.q[p][k0 / 64]), 16) + (k0 % 64) / 8,
-                     kvt_desc(smem_u32(sm.k[slot][k0 / 64]), 16) + (k0 % 64) / 8, is, p > 0 || k0 > 0);
-      kvt_commit(sm.s_full + (j & 1));
+          for (int k0 = 0; k0 < DH; k0 += 16)  // 16 channels: 32 bytes inside the swizzle atom
+            kvt_mma_ss(d, qd + (p * KvtSmem<DH, QP>::HALVES + k0 / 64) * QSTEP + k0 % 64 / 8, kj + k0 / 64 * KSTEP + k0 % 64 / 8, is,
+                       p > 0 || k0 > 0);
+        kvt_commit(sm.s_full + buf);
+      }
+      __syncwarp();
       return true;
     };
     ok = kvt_wait(&sm.q_full, 0) && scores(0);
     for (int j = 0; ok && j < nt; ++j) {
-      // the next tile's scores run under this tile's weights; their columns held P of the tile before
-      if ((j > 0 && !kvt_wait(&sm.o_done, (j - 1) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(&sm.p_full, j & 1)) {
+      // the next tile's scores run under this tile's weights; their columns held P of a tile whose product is done
+      const int b = j + 1 - BUFS;
+      if ((b >= 0 && !kvt_wait(sm.o_done + b % BUFS, (b / BUFS) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(&sm.p_full, j & 1)) {
         ok = false;
         break;
       }
       kvt_after();
-      const int slot = j % SLOTS;
+      const int slot = j % SLOTS, buf = j % BUFS;
+      if (lead) {
+        const uint64_t vj = vd + (uint32_t)slot * KSLOT;
+        const uint32_t pa = tmem + buf * N;
 #pragma unroll
-      for (int p = PP - 1; p >= 0; --p)
+        for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
-        for (int k0 = 0; k0 < N; k0 += 16)  // 16 keys: two 8-row groups of V
-          kvt_mma_ts(tmem + COL_O, tmem + (j & 1) * N + p * (N / 2) + k0 / 2, kvt_desc(smem_u32(sm.v[slot][0]), N * 128) + k0 * 8, io,
-                     j > 0 || p < PP - 1 || k0 > 0);
-      kvt_commit(&sm.o_done);
-      kvt_commit(sm.kv_empty + slot);
+          for (int k0 = 0; k0 < N; k0 += 16)  // 16 keys: two 8-row groups of V
+            kvt_mma_ts(tmem + COL_O, pa + p * (N / 2) + k0 / 2, vj + k0 * 8, io, j > 0 || p < PP - 1 || k0 > 0);
+        kvt_commit(sm.o_done + buf);
+        kvt_commit(sm.kv_empty + slot);
+      }
+      __syncwarp();
     }
-    if (ok) ok = kvt_wait(&sm.o_done, (nt - 1) & 1);  // nothing is in flight when the memory goes
+    if (ok) ok = kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1);  // nothing is in flight when the memory goes
   }
   kvt_before();
   const bool all_ok = __syncthreads_and(ok) != 0;
