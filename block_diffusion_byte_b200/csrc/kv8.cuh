@@ -158,6 +158,19 @@ __device__ __forceinline__ void kv8_ld4(const void* p, int dtype, long long i, b
     x[0] = f.x, x[1] = f.y, x[2] = h.x, x[3] = h.y;
   }
 }
+// Four elements to i; vec: 16-byte aligned rows (i a multiple of 4).
+__device__ __forceinline__ void kv8_st4(void* p, int dtype, long long i, bool vec, float x, float y, float z, float w) {
+  if (!vec) {
+    kv8_st(p, dtype, i, x), kv8_st(p, dtype, i + 1, y), kv8_st(p, dtype, i + 2, z), kv8_st(p, dtype, i + 3, w);
+  } else if (dtype == BLT_T_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x, y, z, w);
+  } else if (dtype == BLT_T_BF16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(f2_to_bf16x2(x, y), f2_to_bf16x2(z, w));
+  } else {
+    const __half2 a = __floats2half2_rn(x, y), b = __floats2half2_rn(z, w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
 // Eight elements from i; vec: 16-byte aligned.
 __device__ __forceinline__ void kv8_ld8(const void* p, int dtype, long long i, bool vec, float (&x)[8]) {
   if (!vec) {

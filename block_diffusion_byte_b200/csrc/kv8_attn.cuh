@@ -474,10 +474,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   auto finish = [&](int qn, int d, float4 v, float M, float L) {
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // nothing visible: 0; NaN stays
     const long long at = (long long)row_of(qn) * a.os + (long long)head_of(qn) * a.ohs + d;
-    kv8_st(a.out, DT, at, v.x * inv);
-    kv8_st(a.out, DT, at + 1, v.y * inv);
-    kv8_st(a.out, DT, at + 2, v.z * inv);
-    kv8_st(a.out, DT, at + 3, v.w * inv);
+    kv8_st4(a.out, DT, at, a.out_vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     if (d == 0 && a.lse) a.lse[(size_t)row_of(qn) * a.Hq + head_of(qn)] = L == 0.f ? -INFINITY : (M + log2f(L)) * ln2;
   };
   for (int i = threadIdx.x; i < nq * (DH / 4); i += kKv8Warps * 32) {
@@ -544,20 +541,20 @@ cudaError_t kv8_attend_one(const Kv8View& c, const Kv8AttnArgs& a, int max_keys,
   at[0].val.clusterDim.x = cl;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cl > 1;
   return cudaLaunchKernelEx(&cfg, kern, c, a, cl);
 }
 
 constexpr int kKv8TileRows = 96;
 template <int DH, int FMT>
-cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t st);
+cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, int max_keys, int sm_count, cudaStream_t st);
 
 template <int DH, int FMT>
 cudaError_t kv8_attend_dh(const Kv8View& c, const Kv8AttnArgs& a, int max_keys, int sm_count, cudaStream_t st) {
   // many rows: tiles of 128 queries on tcgen05
   const long long tiles = ((long long)a.max_rows * a.G + 127) / 128;
-  if (!a.sel_pages && (long long)a.max_rows * a.G >= kKv8TileRows && tiles * c.H * c.batch < INT_MAX)
-    return kv8_tile_dh<DH, FMT>(c, a, tiles, st);
+  if (!a.sel_pages && (long long)a.max_rows * a.G >= kKv8TileRows && tiles * c.H * c.batch <= INT_MAX / 8)
+    return kv8_tile_dh<DH, FMT>(c, a, tiles, max_keys, sm_count, st);
   // queries a tile: 8, or 16 where a tile can hold more than 8
   const bool wide = (a.sel_pages ? a.G : (long long)a.max_rows * a.G) > 8;
   // planes (11 bits each) of the queries and of the weights: fp32 two and two; bf16 and f16 queries fit one; weights one

@@ -17,6 +17,8 @@
 // that time.  Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
 #pragma once
 
+#include <cstddef>
+
 #include "kv8.cuh"
 #include "kv8_attn.cuh"
 
@@ -48,6 +50,11 @@ struct KvtSmem {
   uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH>()], p_full, o_done[kvt_bufs<DH>()];
   uint32_t tmem;
   int max_lim;
+};
+template <int DH>
+struct KvtSums {  // a CTA's sums, in place of the operands
+  float o[kKvtQ][DH + 4];
+  float2 ml[kKvtQ];
 };
 template <int DH, int QP>
 constexpr size_t kvt_smem() { return sizeof(KvtSmem<DH, QP>) + 1024; }
@@ -143,18 +150,19 @@ __device__ __forceinline__ int kvt_swz(int row, int c) { return row * 128 + ((c 
 // prompt) first, so that long CTAs start early.
 template <int DH, int FMT, int QP, int PP>
 __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 ? 2 : 1)
-    k_kv8_tile(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a, const int n_tiles) {
+    k_kv8_tile(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a, const int n_tiles, const int CL) {
   constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH>(), BUFS = kvt_bufs<DH>();
   constexpr int COL_O = BUFS * N;  // tensor memory: tiles of S (P's planes in place, N / 2 columns each), O
   constexpr int DT = QP == 2 ? BLT_T_F32 : PP == 1 ? BLT_T_BF16 : BLT_T_F16;  // a.dtype
   extern __shared__ uint8_t kvt_raw[];
   KvtSmem<DH, QP>& sm = *reinterpret_cast<KvtSmem<DH, QP>*>((reinterpret_cast<uintptr_t>(kvt_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int kvh = blockIdx.x % c.H, s = blockIdx.x / c.H % c.batch, tile = n_tiles - 1 - (int)(blockIdx.x / c.H / c.batch);
+  const int rank = blockIdx.x % CL, item = blockIdx.x / CL;
+  const int kvh = item % c.H, s = item / c.H % c.batch, tile = n_tiles - 1 - item / c.H / c.batch;
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
   const int qbase = tile * kKvtQ, nq = min((r1 - r0) * a.G - qbase, kKvtQ);
-  if (nq <= 0) return;
+  if (nq <= 0) return;  // the same for every CTA of a cluster
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, kKvtQ);
@@ -195,8 +203,11 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
   __syncthreads();
   kvt_after();
   const uint32_t tmem = sm.tmem;
-  const int max_lim = sm.max_lim, nt = (max_lim + N - 1) / N;
+  // this CTA's tiles: j0 .. j0 + nt - 1 of the keys' (the loops below count from 0)
+  const int max_lim = sm.max_lim, all_tiles = (max_lim + N - 1) / N, per = (all_tiles + CL - 1) / CL;
+  const int j0 = min(rank * per, all_tiles), nt = min(per, all_tiles - j0);
   bool ok = true;
+  KvtSums<DH>& sums = *reinterpret_cast<KvtSums<DH>*>(&sm);
 
   if (warp < 4) {
     // ------------------------------------------------------------------ a thread a query
@@ -232,6 +243,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     const float qs = a.scale == 0.f ? 1.f : kv8_pow2(ex - 14) * (fabsf(a.scale) * 1.4426950408889634f);
 #pragma unroll
     for (int c0 = 0; c0 < DH; c0 += QC) {
+      if (nt == 0) break;  // the memory is the sums' at once
       if (QC < DH) fetch(c0);
 #pragma unroll
       for (int i = 0; i < QC; i += 8) {
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
       const int4 meta = sm.meta[slot];
-      const int pos0 = j * N;
+      const int pos0 = (j0 + j) * N;
       const float ks = kv8_pow2(meta.x) * qs;
       const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim) && meta.z == 0;
 #pragma unroll
@@ -329,12 +341,12 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       kvt_before();
       mbar_arrive(&sm.p_full);
     }
-    // ---- out = O / l
+    // ---- the CTA's own sums
     if (nt > 0 && ok && !kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
     kvt_after();
-    if (ok) {
+    if (ok && CL == 1) {  // out = O / l
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // nothing visible: 0; NaN stays
-      const float fin = inv * kv8_pow2(vrun - kKvtShift);
+      const float unit = inv * kv8_pow2(vrun - kKvtShift);
       const long long at = (long long)qrow * a.os + (long long)qhead * a.ohs;
 #pragma unroll
       for (int c0 = 0; c0 < DH; c0 += 32) {
@@ -346,14 +358,30 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         if (mine) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
-            float x[8];
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : v[i + e] * fin;
-            kv8_st8(a.out, DT, at + c0 + i, a.out_vec, x);
+            for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : v[i + e] * unit;
+            kv8_st8(a.out, DT, at + c0 + i, a.out_vec, y);
           }
         }
       }
       if (mine && a.lse) a.lse[(size_t)qrow * a.Hq + qhead] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    } else if (ok) {
+      // for the cluster: over the operands' memory, every product has been made
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      const float unit = kv8_pow2(vrun - kKvtShift);
+      if (nt > 0) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          float v[32];
+          kvt_ld32(lane_base + COL_O + c0, v);
+          kvt_ld_wait(v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(&sums.o[threadIdx.x][c0 + i]) = make_float4(v[i] * unit, v[i + 1] * unit, v[i + 2] * unit, v[i + 3] * unit);
+        }
+      }
+      sums.ml[threadIdx.x] = make_float2(m, l);
     }
   } else if (warp < 7) {
     // ------------------------------------------------------------------ codes to operands
@@ -364,7 +392,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     // lane b < NB: the table's entry for the tile's block b, INT_MIN if it has none.  The entry is looked at when the
     // codes are asked for, a tile later: looking at it here would wait for it.
     auto entry_of = [&](int j) {
-      const int blk = j * NB + lane;
+      const int blk = (j0 + j) * NB + lane;
       if (j >= nt || lane >= NB || blk * kKv8Block >= max_lim) return INT_MIN;
       return __ldg(c.table + (size_t)s * c.max_pages + kv8_div_tpp(c, blk));
     };
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       __syncwarp();
       int ke = -1, ve = -1;
       if (there) {
-        const int blk = j * NB + lane, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
+        const int blk = (j0 + j) * NB + lane, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
         const size_t at = (size_t)entry * c.page_stride + ((size_t)kvh * c.PT + sub * kKv8Block) * DH;
         bulk_g2s(raw_of(sm.k[slot], lane), c.k + at, kKv8Block * DH, sm.raw_full + slot);
         bulk_g2s(raw_of(sm.v[slot], lane), c.v + at, kKv8Block * DH, sm.raw_full + slot);
@@ -436,7 +464,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         break;
       }
       const int kref = max(__reduce_max_sync(0xffffffffu, ke), kKv8LowExp), vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
-      const int rows = min(max_lim - j * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
+      const int rows = min(max_lim - (j0 + j) * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
       // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
       if (lane == 0) sm.meta[slot] = make_int4(kref, vref, (int)(~held & ((1u << nb) - 1)), 0);
       convert(sm.k[slot], kvt_pow2_f16x2(kref - ke), held, N);
@@ -500,23 +528,65 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256));
   }
   if (!all_ok && threadIdx.x == 0 && c.status) set_status(c.status, kErrDevice);
+  if (CL == 1) return;
+  // ---- join the cluster and store: each CTA finishes a share of the rows, four channels a thread
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  const int share = kKvtQ / CL;
+  for (int i = threadIdx.x; all_ok && i < share * (DH / 4); i += kKvtThreads) {
+    const int qn = rank * share + i / (DH / 4), d = i % (DH / 4) * 4;
+    if (qn >= nq) break;
+    float M = -INFINITY, L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < CL; ++r) M = fmaxf(M, cl.map_shared_rank(&sums.ml[qn], r)->x);
+    for (int r = 0; r < CL; ++r) {
+      const float2 ml = *cl.map_shared_rank(&sums.ml[qn], r);
+      if (ml.y == 0.f) continue;  // saw nothing
+      const float f = ml.x == M ? 1.f : ex2(ml.x - M);
+      const float4 x = *reinterpret_cast<const float4*>(cl.map_shared_rank(&sums.o[qn][d], r));
+      L += f * ml.y;
+      v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const int row = r0 + (qbase + qn) / a.G, head = kvh * a.G + (qbase + qn) % a.G;
+    kv8_st4(a.out, DT, (long long)row * a.os + (long long)head * a.ohs + d, a.out_vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (d == 0 && a.lse) a.lse[(size_t)row * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+  cl.sync();  // the others may still read this CTA's sums
 }
 
 template <int DH, int FMT, int QP, int PP>
-cudaError_t kv8_tile_one(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t stream) {
+cudaError_t kv8_tile_one(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, int max_keys, int sm_count, cudaStream_t stream) {
+  using Smem = KvtSmem<DH, QP>;
+  static_assert(sizeof(KvtSums<DH>) <= offsetof(Smem, meta), "the sums fit in the operands' memory");
   auto kern = k_kv8_tile<DH, FMT, QP, PP>;
   constexpr int smem = (int)kvt_smem<DH, QP>();
+  const long long ctas = tiles * c.H * c.batch;
+  // Split the keys over a cluster while all its CTAs still run at once (two an SM) and each keeps 16 tiles.
+  int cl = 1;
+  while (cl < 8 && ctas * cl * 2 <= 2 * sm_count && max_keys >= cl * 2 * 16 * kKvtN) cl *= 2;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(tiles * c.H * c.batch), kKvtThreads, smem, stream>>>(c, a, (int)tiles);
-  return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(ctas * cl));
+  cfg.blockDim = dim3(kKvtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cl;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cl > 1;
+  return cudaLaunchKernelEx(&cfg, kern, c, a, (int)tiles, cl);
 }
 
 template <int DH, int FMT>
-cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, cudaStream_t st) {
-  if (a.dtype == BLT_T_F32) return kv8_tile_one<DH, FMT, 2, 2>(c, a, tiles, st);
-  if (a.dtype == BLT_T_BF16) return kv8_tile_one<DH, FMT, 1, 1>(c, a, tiles, st);
-  return kv8_tile_one<DH, FMT, 1, 2>(c, a, tiles, st);
+cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, int max_keys, int sm_count, cudaStream_t st) {
+  if (a.dtype == BLT_T_F32) return kv8_tile_one<DH, FMT, 2, 2>(c, a, tiles, max_keys, sm_count, st);
+  if (a.dtype == BLT_T_BF16) return kv8_tile_one<DH, FMT, 1, 1>(c, a, tiles, max_keys, sm_count, st);
+  return kv8_tile_one<DH, FMT, 1, 2>(c, a, tiles, max_keys, sm_count, st);
 }
 
 }  // namespace bltdec
