@@ -162,6 +162,7 @@ class blt_kv8_cache(C.Structure):
 
 
 class blt_kv8_rows(C.Structure):
+    fits = None  # the cache these arguments were found to fit
     _fields_ = [
         ("k", C.c_void_p),
         ("v", C.c_void_p),
@@ -177,6 +178,7 @@ class blt_kv8_rows(C.Structure):
 
 
 class blt_kv8_attention(C.Structure):
+    fits = None  # the cache these arguments were found to fit
     _fields_ = [
         ("q", C.c_void_p),
         ("out", C.c_void_p),
@@ -201,6 +203,7 @@ class blt_kv8_attention(C.Structure):
 
 
 class blt_kv8_selection(C.Structure):
+    fits = None  # the cache these arguments were found to fit
     _fields_ = [
         ("q", C.c_void_p),
         ("dtype", C.c_int32),
@@ -558,13 +561,14 @@ def kv8_selection(q, row_offsets, row_limit, max_rows: int, max_keys: int, sel_p
 
 
 def _kv8_call(name: str, cache: blt_kv8_cache, args, stream) -> None:
-    batch, heads, dim = args.shape
-    if batch != cache.batch or dim != cache.head_dim or heads not in (None, cache.n_heads):
-        raise ValueError(f"{name}: arguments for {batch} sequences, {heads} heads of {dim}; the cache has {cache.batch}, {cache.n_heads} of {cache.head_dim}")
-    lib = load_library()
-    rc = getattr(lib, name)(cache, args, stream)
+    if args.fits is not cache:  # looked at once for each pair of descriptors
+        batch, heads, dim = args.shape
+        if batch != cache.batch or dim != cache.head_dim or heads not in (None, cache.n_heads):
+            raise ValueError(f"{name}: arguments for {batch} sequences, {heads} heads of {dim}; the cache has {cache.batch}, {cache.n_heads} of {cache.head_dim}")
+        args.fits = cache
+    rc = getattr(_lib or load_library(), name)(cache, args, stream)
     if rc != BLT_OK:
-        raise BltError(rc, name, lib.blt_kv8_last_error().decode())
+        raise BltError(rc, name, _lib.blt_kv8_last_error().decode())
 
 
 def blt_kv8_append(cache: blt_kv8_cache, rows: blt_kv8_rows, stream: Optional[int] = None) -> None:

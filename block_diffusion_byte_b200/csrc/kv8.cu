@@ -20,14 +20,16 @@ struct Kv8RowsArgs {
   const int *row_off, *start;
 };
 
+constexpr int kKv8RowThreads = 256;  // of append and read, at most
+
 // ------------------------------------------------------------------------ append
-// One CTA per (touched page, head, sequence), one warp per (block of 16 positions, K or V): a lane keeps
-// DH / 16 groups of 8 channels in registers, so a block's rows are read once, its amax is a warp
-// reduction, and the codes leave as 8-byte pieces.
-template <int DH, int FMT>
-__global__ void __launch_bounds__(512) k_kv8_append(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
+// One CTA per touched page of a sequence and one or more heads (grid.y of them share the heads), one warp per (block of
+// 16 positions, K or V): a lane keeps DH / 16 groups of 8 channels in registers, so a block's rows are read once, its
+// amax is a warp reduction, and the codes leave as 8-byte pieces.
+template <int DH, int FMT, int DT>
+__global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
   constexpr int GPR = DH / 8, NG = DH / 16;  // groups per row; groups per lane
-  const int h = blockIdx.y, s = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int s = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
   if (r1 <= r0) return;
@@ -41,105 +43,120 @@ __global__ void __launch_bounds__(512) k_kv8_append(const __grid_constant__ Kv8V
   if (p0 >= end) return;
   const int page = kv8_page(c, s, pi);
   if (page < 0) return;
-  const size_t at = (size_t)page * c.page_stride + (size_t)h * c.PT * DH;
-  const size_t ex = (size_t)page * c.exp_stride + (size_t)h * c.tpp;
   const int b0 = max(start - p0, 0) / kKv8Block, b1 = (min(end - p0, c.PT) + kKv8Block - 1) / kKv8Block;  // blocks that take rows
-  for (int i = warp; i < 2 * (b1 - b0); i += nw) {
-    const bool val = i & 1;
-    const int b = b0 + (i >> 1), q0 = p0 + b * kKv8Block;
-    uint8_t* codes = (val ? c.v : c.k) + at + (size_t)b * kKv8Block * DH;
-    uint8_t* exps = (val ? c.ve : c.ke) + ex + b;
-    const void* src = val ? a.v : a.k;
-    float x[NG][8];
-    float old = 0.f;
-    if (q0 < start) old = kv8_pow2(*exps);  // kept rows: all lanes read the exponent before lane 0 writes it
-    float amax = 0.f;
+  __shared__ float lo[16][DH], hi[16][DH];
+  __shared__ float s_amax[kKv8RowThreads / 32];
+#pragma unroll 1
+  for (int h = blockIdx.y; h < c.H; h += gridDim.y) {
+    const size_t at = (size_t)page * c.page_stride + (size_t)h * c.PT * DH;
+    const size_t ex = (size_t)page * c.exp_stride + (size_t)h * c.tpp;
+    for (int i = warp; i < 2 * (b1 - b0); i += nw) {
+      const bool val = i & 1;
+      const int b = b0 + (i >> 1), q0 = p0 + b * kKv8Block;
+      uint8_t* codes = (val ? c.v : c.k) + at + (size_t)b * kKv8Block * DH;
+      uint8_t* exps = (val ? c.ve : c.ke) + ex + b;
+      const void* src = val ? a.v : a.k;
+      float x[NG][8];
+      float old = 0.f;
+      if (q0 < start) old = kv8_pow2(*exps);  // kept rows: all lanes read the exponent before lane 0 writes it
+      if (q0 >= start && q0 + kKv8Block <= end && a.vec) {  // a block of new rows: all its loads at once
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const int gi = j * 32 + lane, pos = q0 + gi / GPR, ch = gi % GPR * 8;
-      if (pos < start) {
-        kv8_decode8<FMT>(*reinterpret_cast<const uint2*>(codes + gi * 8), x[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] *= old;
-      } else if (pos < end) {
-        kv8_ld8(src, a.dtype, (long long)(r0 + pos - start) * a.rs + (long long)h * a.hs + ch, a.vec, x[j]);
+        for (int j = 0; j < NG; ++j) {
+          const int gi = j * 32 + lane;
+          kv8_ld8(src, DT, (long long)(r0 + q0 + gi / GPR - start) * a.rs + (long long)h * a.hs + gi % GPR * 8, true, x[j]);
+        }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
+        for (int j = 0; j < NG; ++j) {
+          const int gi = j * 32 + lane, pos = q0 + gi / GPR, ch = gi % GPR * 8;
+          if (pos < start) {
+            kv8_decode8<FMT>(*reinterpret_cast<const uint2*>(codes + gi * 8), x[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] *= old;
+          } else if (pos < end) {
+            kv8_ld8(src, DT, (long long)(r0 + pos - start) * a.rs + (long long)h * a.hs + ch, a.vec, x[j]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
+          }
+        }
       }
+      float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, kv8_mag(x[j][e]));
-    }
-    amax = warp_max(amax);
-    const int e = kv8_exponent<FMT>(amax);
-    const float inv = kv8_pow2(254 - e);
+      for (int j = 0; j < NG; ++j)
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      const int gi = j * 32 + lane, pos = q0 + gi / GPR;
-      if (pos < end) {
-        uint2 w;
-        w.x = kv8_encode4<FMT>(x[j][0], x[j][1], x[j][2], x[j][3], inv);
-        w.y = kv8_encode4<FMT>(x[j][4], x[j][5], x[j][6], x[j][7], inv);
-        *reinterpret_cast<uint2*>(codes + gi * 8) = w;
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, kv8_mag(x[j][e]));
+      amax = warp_max(amax);
+      const int e = kv8_exponent<FMT>(amax);
+      const float inv = kv8_pow2(254 - e);
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const int gi = j * 32 + lane, pos = q0 + gi / GPR;
+        if (pos < end) {
+          uint2 w;
+          w.x = kv8_encode4<FMT>(x[j][0], x[j][1], x[j][2], x[j][3], inv);
+          w.y = kv8_encode4<FMT>(x[j][4], x[j][5], x[j][6], x[j][7], inv);
+          *reinterpret_cast<uint2*>(codes + gi * 8) = w;
+        }
       }
+      __syncwarp();
+      if (lane == 0) *exps = (uint8_t)e;
     }
-    __syncwarp();
-    if (lane == 0) *exps = (uint8_t)e;
-  }
-  if (!c.kmin) return;
-  // ---- the page's summary over every position it holds now
-  __shared__ float lo[16][DH], hi[16][DH];
-  __shared__ float s_amax[16];
-  __syncthreads();  // the codes and exponents of this page are the CTA's own writes
-  const int held = min(end - p0, c.PT);
-  {
-    // thread: channels 8 (i % GPR) .., positions i / GPR, i / GPR + step, ...
-    const int lanes = min((int)blockDim.x / GPR, 16), row = threadIdx.x / GPR, ch = threadIdx.x % GPR * 8;
-    if (row < lanes) {
-      float mn[8], mx[8];
+    if (!c.kmin) continue;
+    // ---- the page's summary over every position it holds now
+    __syncthreads();  // the codes and exponents of this page are the CTA's own writes
+    const int held = min(end - p0, c.PT);
+    {
+      // thread: channels 8 (i % GPR) .., positions i / GPR, i / GPR + step, ...
+      const int lanes = min((int)blockDim.x / GPR, 16), row = threadIdx.x / GPR, ch = threadIdx.x % GPR * 8;
+      if (row < lanes) {
+        float mn[8], mx[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mn[e] = INFINITY, mx[e] = -INFINITY;
-      for (int p = row; p < held; p += lanes) {
-        float y[8];
-        kv8_decode8<FMT>(*reinterpret_cast<const uint2*>(c.k + at + (size_t)p * DH + ch), y);
-        const float sc = kv8_pow2(c.ke[ex + p / kKv8Block]);
+        for (int e = 0; e < 8; ++e) mn[e] = INFINITY, mx[e] = -INFINITY;
+        for (int p = row; p < held; p += lanes) {
+          float y[8];
+          kv8_decode8<FMT>(*reinterpret_cast<const uint2*>(c.k + at + (size_t)p * DH + ch), y);
+          const float sc = kv8_pow2(c.ke[ex + p / kKv8Block]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mn[e] = fminf(mn[e], y[e] * sc), mx[e] = fmaxf(mx[e], y[e] * sc);
+          for (int e = 0; e < 8; ++e) mn[e] = fminf(mn[e], y[e] * sc), mx[e] = fmaxf(mx[e], y[e] * sc);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lo[row][ch + e] = mn[e], hi[row][ch + e] = mx[e];
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lo[row][ch + e] = mn[e], hi[row][ch + e] = mx[e];
+      __syncthreads();
+      float amax = 0.f;
+      for (int d = threadIdx.x; d < DH; d += blockDim.x) {
+        float mn = lo[0][d], mx = hi[0][d];
+        for (int r = 1; r < lanes; ++r) mn = fminf(mn, lo[r][d]), mx = fmaxf(mx, hi[r][d]);
+        // a code's value can lie beyond fp32 where a block holds magnitudes near 3e38: it counts as fp32's largest
+        mn = fminf(fmaxf(mn, -FLT_MAX), FLT_MAX), mx = fminf(fmaxf(mx, -FLT_MAX), FLT_MAX);
+        lo[0][d] = mn, hi[0][d] = mx;
+        amax = fmaxf(amax, fmaxf(fabsf(mn), fabsf(mx)));
+      }
+      amax = warp_max(amax);
+      if (lane == 0) s_amax[warp] = amax;
+      __syncthreads();
+      amax = s_amax[0];
+      for (int w = 1; w < nw; ++w) amax = fmaxf(amax, s_amax[w]);
+      const int e = kv8_exponent<0>(amax);
+      const float inv = kv8_pow2(254 - e);
+      for (int d = threadIdx.x; d < DH; d += blockDim.x) {
+        const size_t o = (size_t)page * c.sum_stride + (size_t)h * DH + d;
+        c.kmin[o] = (int8_t)__float2int_rn(lo[0][d] * inv);
+        c.kmax[o] = (int8_t)__float2int_rn(hi[0][d] * inv);
+      }
+      if (threadIdx.x == 0) c.ksexp[(size_t)page * c.sexp_stride + h] = (uint8_t)e;
+      __syncthreads();  // the next head writes the shared arrays
     }
-    __syncthreads();
-    float amax = 0.f;
-    for (int d = threadIdx.x; d < DH; d += blockDim.x) {
-      float mn = lo[0][d], mx = hi[0][d];
-      for (int r = 1; r < lanes; ++r) mn = fminf(mn, lo[r][d]), mx = fmaxf(mx, hi[r][d]);
-      // a code's value can lie beyond fp32 where a block holds magnitudes near 3e38: it counts as fp32's largest
-      mn = fminf(fmaxf(mn, -FLT_MAX), FLT_MAX), mx = fminf(fmaxf(mx, -FLT_MAX), FLT_MAX);
-      lo[0][d] = mn, hi[0][d] = mx;
-      amax = fmaxf(amax, fmaxf(fabsf(mn), fabsf(mx)));
-    }
-    amax = warp_max(amax);
-    if (lane == 0) s_amax[warp] = amax;
-    __syncthreads();
-    amax = s_amax[0];
-    for (int w = 1; w < nw; ++w) amax = fmaxf(amax, s_amax[w]);
-    const int e = kv8_exponent<0>(amax);
-    const float inv = kv8_pow2(254 - e);
-    for (int d = threadIdx.x; d < DH; d += blockDim.x) {
-      const size_t o = (size_t)page * c.sum_stride + (size_t)h * DH + d;
-      c.kmin[o] = (int8_t)__float2int_rn(lo[0][d] * inv);
-      c.kmax[o] = (int8_t)__float2int_rn(hi[0][d] * inv);
-    }
-    if (threadIdx.x == 0) c.ksexp[(size_t)page * c.sexp_stride + h] = (uint8_t)e;
   }
 }
 
 // ------------------------------------------------------------------------ read
-template <int DH, int FMT>
-__global__ void __launch_bounds__(512) k_kv8_read(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
-  constexpr int GPR = DH / 8;
-  const int h = blockIdx.y, s = blockIdx.z;
+// The same grid; a thread takes pieces of 8 codes, four in flight.
+template <int DH, int FMT, int DT>
+__global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_read(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
+  constexpr int GPR = DH / 8, UN = 4;
+  const int s = blockIdx.z;
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
   if (r1 <= r0) return;
@@ -152,18 +169,39 @@ __global__ void __launch_bounds__(512) k_kv8_read(const __grid_constant__ Kv8Vie
   const int end = start + (r1 - r0), pi = start / c.PT + blockIdx.x, p0 = pi * c.PT;
   if (p0 >= end) return;
   const int page = kv8_page(c, s, pi);
-  const int q0 = max(p0, start), n = min(end, p0 + c.PT) - q0;
-  for (int i = threadIdx.x; i < 2 * n * GPR; i += blockDim.x) {
-    const bool val = i >= n * GPR;
-    const int gi = val ? i - n * GPR : i, pos = q0 + gi / GPR, ch = gi % GPR * 8, in = pos - p0;
-    float x[8] = {};
-    if (page >= 0) {
-      kv8_decode8<FMT>(*reinterpret_cast<const uint2*>((val ? c.v : c.k) + (size_t)page * c.page_stride + ((size_t)h * c.PT + in) * DH + ch), x);
-      const float sc = kv8_pow2((val ? c.ve : c.ke)[(size_t)page * c.exp_stride + (size_t)h * c.tpp + in / kKv8Block]);
+  const int q0 = max(p0, start), n = min(end, p0 + c.PT) - q0, half = n * GPR;
+#pragma unroll 1
+  for (int h = blockIdx.y; h < c.H; h += gridDim.y) {
+    const size_t at = (size_t)page * c.page_stride + (size_t)h * c.PT * DH, ex = (size_t)page * c.exp_stride + (size_t)h * c.tpp;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < 2 * half; i0 += UN * blockDim.x) {
+      uint2 w[UN];
+      int e[UN];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= sc;
+      for (int u = 0; u < UN; ++u) {
+        const int i = i0 + u * blockDim.x;
+        w[u] = make_uint2(0, 0);
+        e[u] = 127;
+        if (page >= 0 && i < 2 * half) {
+          const bool val = i >= half;
+          const int gi = val ? i - half : i, in = q0 + gi / GPR - p0;
+          w[u] = __ldg(reinterpret_cast<const uint2*>((val ? c.v : c.k) + at + (size_t)in * DH + gi % GPR * 8));
+          e[u] = __ldg((val ? c.ve : c.ke) + ex + in / kKv8Block);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int i = i0 + u * blockDim.x;
+        if (i >= 2 * half) break;
+        const bool val = i >= half;
+        const int gi = val ? i - half : i;
+        float x[8];
+        kv8_decode8<FMT>(w[u], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= kv8_pow2(e[u]);
+        kv8_st8(val ? a.v : a.k, DT, (long long)(r0 + q0 + gi / GPR - start) * a.rs + (long long)h * a.hs + gi % GPR * 8, a.vec, x);
+      }
     }
-    kv8_st8(val ? a.v : a.k, a.dtype, (long long)(r0 + pos - start) * a.rs + (long long)h * a.hs + ch, a.vec, x);
   }
 }
 
@@ -176,7 +214,7 @@ struct Kv8SelArgs {
   int *pages, *count;
 };
 
-constexpr int kKv8SelThreads = 512;
+constexpr int kKv8SelThreads = 512;  // at most
 
 // One CTA per (row, key/value head).  Scores: four lanes share a page's minima and maxima; a query channel
 // is either >= 0 or < 0, so max(q lo, q hi) is q's positive part times the maximum plus its negative part
@@ -185,13 +223,15 @@ constexpr int kKv8SelThreads = 512;
 template <int DH>
 __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8SelArgs a) {
   constexpr int QW = DH / 4, LW = DH / 16;  // words of a row; words of a lane
-  constexpr int NW = kKv8SelThreads / 32;
+  constexpr int NWMAX = kKv8SelThreads / 32;
+  constexpr int BATCH = DH <= 64 ? 4 : 2;  // pages a lane has in flight
   extern __shared__ uint32_t sel_smem[];
   __shared__ uint32_t hist[256];
-  __shared__ int warp_n[NW][2];
+  __shared__ int warp_n[NWMAX][2];
   __shared__ uint32_t s_prefix;
   __shared__ int s_left;
   const int s = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int T = blockDim.x, NW = T >> 5;
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
   const int row = r0 + blockIdx.x;
@@ -209,9 +249,15 @@ __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_cons
   int* out = a.pages + ((size_t)row * c.H + kvh) * a.n_select;
   if (threadIdx.x == 0) a.count[(size_t)row * c.H + kvh] = min(nb, a.n_select);
   if (nb <= a.n_select) {
-    for (int i = threadIdx.x; i < a.n_select; i += kKv8SelThreads) out[i] = i < nb ? i : -1;
+    for (int i = threadIdx.x; i < a.n_select; i += T) out[i] = i < nb ? i : -1;
     return;
   }
+  // the first pages' table entries are on their way while the queries are made
+  const int t = lane & 3, stride = NW * 8;
+  auto entry = [&](int p) { return p < nb && !(p < a.n_sink || p >= nb - a.n_local) ? __ldg(c.table + (size_t)s * c.max_pages + p) : INT_MIN; };
+  int next[BATCH];
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k) next[k] = entry(warp * 8 + (lane >> 2) + k * stride);
   // ---- the group's queries in 8 bits: a warp a head
   for (int g = warp; g < a.G; g += NW) {
     const long long base = (long long)row * a.qs + (long long)(kvh * a.G + g) * a.qhs;
@@ -236,51 +282,61 @@ __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_cons
   }
   __syncthreads();
   // ---- scores
-  const int t = lane & 3;
-  for (int p = warp * 8 + (lane >> 2); p - (lane >> 2) < nb; p += NW * 8) {
-    const bool forced = p < a.n_sink || p >= nb - a.n_local;
-    float best = -INFINITY;
-    const int page = p < nb && !forced ? kv8_page(c, s, p) : -1;
-    uint32_t lo[LW], hi[LW];
-    float es = 0.f;
-    if (page >= 0) {
-      const size_t o = (size_t)page * c.sum_stride + (size_t)kvh * DH + t * (DH / 4);
+  for (int p0 = warp * 8 + (lane >> 2); p0 - (lane >> 2) < nb; p0 += BATCH * stride) {
+    uint32_t lo[BATCH][LW], hi[BATCH][LW];
+    float es[BATCH];
 #pragma unroll
-      for (int i = 0; i < LW; i += 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.kmin + o + i * 4)), y = __ldg(reinterpret_cast<const uint2*>(c.kmax + o + i * 4));
-        lo[i] = x.x, lo[i + 1] = x.y, hi[i] = y.x, hi[i + 1] = y.y;
+    for (int k = 0; k < BATCH; ++k) {
+      const int page = next[k];
+      const bool there = (unsigned)page < (unsigned)c.n_pages;
+      es[k] = -1.f;  // no page
+#pragma unroll
+      for (int i = 0; i < LW; ++i) lo[k][i] = hi[k][i] = 0;
+      if (there) {
+        const size_t o = (size_t)page * c.sum_stride + (size_t)kvh * DH + t * (DH / 4);
+#pragma unroll
+        for (int i = 0; i < LW; i += 2) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.kmin + o + i * 4)), y = __ldg(reinterpret_cast<const uint2*>(c.kmax + o + i * 4));
+          lo[k][i] = x.x, lo[k][i + 1] = x.y, hi[k][i] = y.x, hi[k][i + 1] = y.y;
+        }
+        es[k] = kv8_pow2(__ldg(c.ksexp + (size_t)page * c.sexp_stride + kvh));
+      } else if (page != INT_MIN && c.status) {
+        set_status(c.status, kErrDevice);
       }
-      es = kv8_pow2(__ldg(c.ksexp + (size_t)page * c.sexp_stride + kvh));
-    } else {
-#pragma unroll
-      for (int i = 0; i < LW; ++i) lo[i] = hi[i] = 0;
     }
-    for (int g = 0; g < a.G; ++g) {
-      int dot = 0;
 #pragma unroll
-      for (int i = 0; i < LW; ++i) {
-        dot = __dp4a((int)qpos[g * QW + t * LW + i], (int)hi[i], dot);
-        dot = __dp4a((int)qneg[g * QW + t * LW + i], (int)lo[i], dot);
+    for (int k = 0; k < BATCH; ++k) next[k] = entry(p0 + (BATCH + k) * stride);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int p = p0 + k * stride;
+      float best = -INFINITY;
+      for (int g = 0; g < a.G; ++g) {
+        int dot = 0;
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+          dot = __dp4a((int)qpos[g * QW + t * LW + i], (int)hi[k][i], dot);
+          dot = __dp4a((int)qneg[g * QW + t * LW + i], (int)lo[k][i], dot);
+        }
+        dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+        dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+        // clamped to fp32's range, so that only pages that are always chosen have an infinite score
+        best = fmaxf(best, fminf(fmaxf((float)dot * qsc[g] * es[k], -FLT_MAX), FLT_MAX));
       }
-      dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-      dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-      // clamped to fp32's range, so that only pages that are always chosen have an infinite score
-      best = fmaxf(best, fminf(fmaxf((float)dot * qsc[g] * es, -FLT_MAX), FLT_MAX));
-    }
-    if (t == 0 && p < nb) {
-      if (forced) best = INFINITY;
-      else if (page < 0) best = -INFINITY;
-      const uint32_t u = __float_as_uint(best + 0.f);  // -0 counts as 0
-      key[p] = u & 0x80000000u ? ~u : u | 0x80000000u;
+      if (t == 0 && p < nb) {
+        if (p < a.n_sink || p >= nb - a.n_local) best = INFINITY;
+        else if (es[k] < 0.f) best = -INFINITY;
+        const uint32_t u = __float_as_uint(best + 0.f);  // -0 counts as 0
+        key[p] = u & 0x80000000u ? ~u : u | 0x80000000u;
+      }
     }
   }
   // ---- the key of the n_select-th page: 8 bits at a time
   if (threadIdx.x == 0) s_prefix = 0, s_left = a.n_select;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 256; i += T) hist[i] = 0;
     __syncthreads();
     const uint32_t prefix = s_prefix;
-    for (int p = threadIdx.x; p - threadIdx.x < nb; p += kKv8SelThreads) {
+    for (int p = threadIdx.x; p - threadIdx.x < nb; p += T) {
       const bool in = p < nb && (shift == 24 || key[p] >> (shift + 8) == prefix >> (shift + 8));
       const unsigned bin = in ? (key[p] >> shift) & 255u : 256u;
       const unsigned same = __match_any_sync(0xffffffffu, bin);  // one atomic per distinct value of a warp
@@ -318,7 +374,7 @@ __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_cons
   const uint32_t kth = s_prefix;
   const int ties = s_left;
   int n_out = 0, n_tie = 0;
-  for (int p0 = 0; p0 < nb; p0 += kKv8SelThreads) {
+  for (int p0 = 0; p0 < nb; p0 += T) {
     const int p = p0 + threadIdx.x;
     const uint32_t k = p < nb ? key[p] : 0;
     const bool eq = p < nb && k == kth, gt = p < nb && k > kth;
@@ -486,7 +542,9 @@ struct AppendLaunch {
   cudaStream_t st;
   template <int DH, int FMT>
   int operator()() const {
-    k_kv8_append<DH, FMT><<<grid, threads, 0, st>>>(v, a);
+    if (a.dtype == BLT_T_F32) k_kv8_append<DH, FMT, BLT_T_F32><<<grid, threads, 0, st>>>(v, a);
+    else if (a.dtype == BLT_T_BF16) k_kv8_append<DH, FMT, BLT_T_BF16><<<grid, threads, 0, st>>>(v, a);
+    else k_kv8_append<DH, FMT, BLT_T_F16><<<grid, threads, 0, st>>>(v, a);
     return 0;
   }
 };
@@ -498,7 +556,9 @@ struct ReadLaunch {
   cudaStream_t st;
   template <int DH, int FMT>
   int operator()() const {
-    k_kv8_read<DH, FMT><<<grid, threads, 0, st>>>(v, a);
+    if (a.dtype == BLT_T_F32) k_kv8_read<DH, FMT, BLT_T_F32><<<grid, threads, 0, st>>>(v, a);
+    else if (a.dtype == BLT_T_BF16) k_kv8_read<DH, FMT, BLT_T_BF16><<<grid, threads, 0, st>>>(v, a);
+    else k_kv8_read<DH, FMT, BLT_T_F16><<<grid, threads, 0, st>>>(v, a);
     return 0;
   }
 };
@@ -506,13 +566,14 @@ struct SelectLaunch {
   const Kv8View& v;
   const Kv8SelArgs& a;
   dim3 grid;
+  int threads;
   size_t smem;
   cudaStream_t st;
   template <int DH, int FMT>
   int operator()() const {
-    const cudaError_t e = cudaFuncSetAttribute(k_kv8_select<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = kv8_allow_smem<k_kv8_select<DH>>(kKv8MaxSelPages * 4 + 64 * (DH / 4 * 8 + 4));
     if (e != cudaSuccess) return cuda_bad("blt_kv8_select", e);
-    k_kv8_select<DH><<<grid, kKv8SelThreads, smem, st>>>(v, a);
+    k_kv8_select<DH><<<grid, threads, smem, st>>>(v, a);
     return 0;
   }
 };
@@ -533,10 +594,15 @@ int store_or_read(const blt_kv8_cache* c, const blt_kv8_rows* rows, void* stream
   if (int rc = dev.enter(c->k)) return rc;
   // rows at any position touch at most this many pages
   const long long pages = ((long long)a.max_rows + 2ll * c->page_tokens - 2) / c->page_tokens;
-  const dim3 grid((unsigned)(pages < c->max_pages ? pages : c->max_pages), (unsigned)c->n_heads, (unsigned)c->batch);
+  const long long px = pages < c->max_pages ? pages : c->max_pages;
+  // Heads share CTAs once there would be more than 16 CTAs an SM: the lookups of a CTA then serve more rows (four prompts
+  // of 8192 rows, 16 heads: append 61 us with a CTA a head, 53 us so; 64 sequences of 16 rows: 8.3 us, 10.5 us with 8 an SM).
+  long long gy = c->n_heads;
+  while (gy > 1 && px * c->batch * gy > 16ll * sm_count()) gy = (gy + 1) / 2;
+  const dim3 grid((unsigned)px, (unsigned)gy, (unsigned)c->batch);
   const int blocks = c->page_tokens / 16, touched = (a.max_rows + 30) / 16;
   int warps = 2 * (blocks < touched ? blocks : touched);
-  warps = warps < 4 ? 4 : warps > 16 ? 16 : warps;
+  warps = warps < 4 ? 4 : warps > kKv8RowThreads / 32 ? kKv8RowThreads / 32 : warps;
   if (store) by_dim(c->head_dim, c->format, AppendLaunch{v, a, grid, warps * 32, (cudaStream_t)stream});
   else by_dim(c->head_dim, c->format, ReadLaunch{v, a, grid, warps * 32, (cudaStream_t)stream});
   return launched(store ? "blt_kv8_append" : "blt_kv8_read");
@@ -621,7 +687,11 @@ int blt_kv8_select(const blt_kv8_cache* c, const blt_kv8_selection* t, void* str
   a.pages = t->sel_pages, a.count = t->sel_count;
   const size_t smem = (size_t)a.G * (c->head_dim / 4) * 8 + ((a.G + 3) & ~3) * 4 + (size_t)c->max_pages * 4;
   const dim3 grid((unsigned)max_rows, (unsigned)c->n_heads, (unsigned)c->batch);
-  if (int rc = by_dim(c->head_dim, c->format, SelectLaunch{v, a, grid, smem, (cudaStream_t)stream})) return rc;
+  // a thread for each expected page, 128 to 512: short lists leave room for more CTAs on an SM (64 rows x 16 heads of 128
+  // pages: 25 us with 512 threads)
+  const int want = (t->max_keys + c->page_tokens - 1) / c->page_tokens;
+  const int threads = want <= 128 ? 128 : want <= 256 ? 256 : kKv8SelThreads;
+  if (int rc = by_dim(c->head_dim, c->format, SelectLaunch{v, a, grid, threads, smem, (cudaStream_t)stream})) return rc;
   return launched("blt_kv8_select");
 }
 

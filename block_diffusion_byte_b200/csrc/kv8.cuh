@@ -10,6 +10,8 @@
 #include <cuda_fp8.h>
 #include <limits.h>
 
+#include <atomic>
+
 #include "bltkv8.h"
 #include "common.cuh"
 
@@ -237,6 +239,18 @@ struct Kv8AttnArgs {
   int n_select;
   int q_vec, out_vec;  // rows of q (out) allow 16-byte loads (stores)
 };
+// Allows a kernel `bytes` of dynamic shared memory on the current device: asked of the driver once a device.
+template <auto KERN>
+cudaError_t kv8_allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 cudaError_t kv8_attend_launch(int fmt, int dh, const Kv8View& c, const Kv8AttnArgs& a, int max_keys, cudaStream_t st);
 
 }  // namespace bltdec

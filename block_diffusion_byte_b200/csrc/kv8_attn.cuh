@@ -48,33 +48,42 @@ __device__ __forceinline__ int kv8_vdim(int b, int g) {
   return (b / VB) * 8 * VB + g * VB + b % VB;
 }
 
+// A unit in shared memory: rows of keys (values) as they come, 16-byte pieces moved about inside each 128 bytes so that
+// the lanes of a load meet different banks.  K: lanes read pieces t of rows g; V: pieces g / 2 or g of rows 2t.
 template <int DH>
-__device__ __forceinline__ void kv8_load_krow(uint32_t (&w)[DH / 16], const uint8_t* row, int t) {
+__device__ __forceinline__ int kv8_kplace(int piece) {  // of piece row * DH / 16 + column
+  return DH == 128 ? piece ^ ((piece >> 3 & 1) << 2) : piece;
+}
+template <int DH>
+__device__ __forceinline__ int kv8_vplace(int piece) {
+  return DH % 64 == 0 ? piece ^ ((piece / (DH / 8) & 3) << 1) : piece;
+}
+template <int DH>
+__device__ __forceinline__ void kv8_load_krow(uint32_t (&w)[DH / 16], const uint8_t* unit, int row, int t) {
   constexpr int CB = kv8_kpiece<DH>();
 #pragma unroll
   for (int i = 0; i < DH / 16; i += CB / 4) {
-    const uint8_t* p = row + kv8_kdim<DH>(i, t);
     if constexpr (CB == 16) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      const uint4 x = *reinterpret_cast<const uint4*>(unit + kv8_kplace<DH>(row * (DH / 16) + kv8_kdim<DH>(i, t) / 16) * 16);
       w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
     } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      const uint2 x = *reinterpret_cast<const uint2*>(unit + row * DH + kv8_kdim<DH>(i, t));
       w[i] = x.x, w[i + 1] = x.y;
     }
   }
 }
 template <int DH>
-__device__ __forceinline__ void kv8_load_vrow(uint32_t (&w)[DH / 32], const uint8_t* row, int g) {
+__device__ __forceinline__ void kv8_load_vrow(uint32_t (&w)[DH / 32], const uint8_t* unit, int row, int g) {
   constexpr int VB = kv8_vpiece<DH>();
   if constexpr (VB == 16) {
-    const uint4 x = *reinterpret_cast<const uint4*>(row + g * 16);
+    const uint4 x = *reinterpret_cast<const uint4*>(unit + kv8_vplace<DH>(row * 8 + g) * 16);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   } else if constexpr (VB == 8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(row + g * 8);
+    const uint2 x = *reinterpret_cast<const uint2*>(unit + kv8_vplace<DH>(row * 4 + (g >> 1)) * 16 + (g & 1) * 8);
     w[0] = x.x, w[1] = x.y;
   } else {
 #pragma unroll
-    for (int j = 0; j < DH / 32; ++j) w[j] = *reinterpret_cast<const uint32_t*>(row + j * 32 + g * 4);
+    for (int j = 0; j < DH / 32; ++j) w[j] = *reinterpret_cast<const uint32_t*>(unit + row * DH + j * 32 + g * 4);
   }
 }
 
@@ -146,17 +155,25 @@ template <int DH>
 __host__ __device__ constexpr int kv8_units() { return DH <= 64 ? 2 : 1; }  // units per step: 4 KB (2 KB for DH 32)
 
 template <int DH, int NQ>
-struct Kv8Smem {
+struct alignas(16) Kv8WarpSmem {
   static constexpr int OS = DH + 4;  // row stride of a partial output (floats): breaks bank alignment of the rows
   union {
-    uint8_t ring[kKv8Warps][kKv8Stages][kv8_units<DH>()][2][kKv8Block * DH];
-    float o[kKv8Warps][8 * NQ][OS];
+    uint8_t ring[kKv8Stages][kv8_units<DH>()][2][kKv8Block * DH];
+    float o[8 * NQ][OS];
   };
-  int2 meta[kKv8Warps][kKv8Stages][kv8_units<DH>()];  // position and exponents (keys' | values' << 8) of a staged unit
-  float m[kKv8Warps][8 * NQ], l[kKv8Warps][8 * NQ];
-  float bo[8 * NQ][OS];  // the CTA's own sums, read by the cluster
-  float bm[8 * NQ], bl[8 * NQ];
+  int2 meta[kKv8Stages][kv8_units<DH>()];  // position and exponents (keys' | values' << 8) of a staged unit
+  float m[8 * NQ], l[8 * NQ];
 };
+template <int DH, int NQ>
+struct alignas(16) Kv8Smem {
+  float bo[8 * NQ][DH + 4];  // the CTA's own sums, read by the cluster
+  float bm[8 * NQ], bl[8 * NQ];
+  Kv8WarpSmem<DH, NQ> w[1];  // of each warp
+};
+template <int DH, int NQ>
+constexpr size_t kv8_smem(int warps) {
+  return sizeof(Kv8Smem<DH, NQ>) + (warps - 1) * sizeof(Kv8WarpSmem<DH, NQ>);
+}
 
 // Registers decide the CTAs an SM holds: two where a lane's queries and outputs leave room.
 template <int DH, int QP, int NQ>
@@ -172,7 +189,8 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   extern __shared__ float4 kv8_smem4[];
   Kv8Smem<DH, NQ>& sm = *reinterpret_cast<Kv8Smem<DH, NQ>*>(kv8_smem4);
   const int tile = blockIdx.x / CL, rank = blockIdx.x % CL, kvh = blockIdx.y, s = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, W = blockDim.x >> 5;
+  Kv8WarpSmem<DH, NQ>& mine = sm.w[warp];
 
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
@@ -218,12 +236,12 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   }
   const int per = ((nu + CL - 1) / CL + U - 1) / U * U;
   const int u0 = min(rank * per, nu), u1 = min(nu, u0 + per);
-  const int steps = max(0, (u1 - u0 + U - 1) / U - warp + kKv8Warps - 1) / kKv8Warps;
+  const int steps = max(0, (u1 - u0 + U - 1) / U - warp + W - 1) / W;
 
   // pages, positions and exponents of the warp's next 32 units, one per lane
   int c_page = -1, c_pos = kKv8NoPos, c_ex = 0;
   auto resolve = [&](int it0) {
-    const int u = u0 + (warp + kKv8Warps * (it0 + lane / U)) * U + lane % U;
+    const int u = u0 + (warp + W * (it0 + lane / U)) * U + lane % U;
     c_page = -1;
     c_pos = kKv8NoPos;
     c_ex = 127;
@@ -254,11 +272,11 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
         if (page < 0) continue;
         const int blk = pos / kKv8Block, sub = blk - kv8_div_tpp(c, blk) * c.tpp;
         const size_t at = (size_t)page * c.page_stride + ((size_t)kvh * c.PT + sub * kKv8Block) * DH;
-        uint8_t* dst = sm.ring[warp][slot][u][0];
+        uint8_t* dst = mine.ring[slot][u][0];
 #pragma unroll
         for (int i = lane; i < DH; i += 32) {
-          cp_async16(dst + i * 16, c.k + at + i * 16, 16);
-          cp_async16(dst + kKv8Block * DH + i * 16, c.v + at + i * 16, 16);
+          cp_async16(dst + kv8_kplace<DH>(i) * 16, c.k + at + i * 16, 16);
+          cp_async16(dst + kKv8Block * DH + kv8_vplace<DH>(i) * 16, c.v + at + i * 16, 16);
         }
       }
     }
@@ -268,7 +286,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     if (it >= steps) return;
     const int src = (it * U + lane) & 31;
     const int pos = __shfl_sync(0xffffffffu, c_pos, src), ex = __shfl_sync(0xffffffffu, c_ex, src);
-    if (lane < U) sm.meta[warp][slot][lane] = make_int2(pos, ex);
+    if (lane < U) mine.meta[slot][lane] = make_int2(pos, ex);
   };
   for (int i = 0; i < S - 1; ++i) issue(i, i);
   for (int i = 0; i < S - 1; ++i) note(i, i);
@@ -327,18 +345,19 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     int vmax = vref;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int2 meta = sm.meta[warp][slot][u];
+      const int2 meta = mine.meta[slot][u];
       pos[u] = meta.x;
       ve[u] = meta.y >> 8;
       vmax = max(vmax, ve[u]);
-      const uint8_t* kp = sm.ring[warp][slot][u][0];
+      const uint8_t* kp = mine.ring[slot][u][0];
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[u][n][e] = 0.f;
+      float odd[4] = {0.f, 0.f, 0.f, 0.f};  // one query group: two chains of products, as no other work stands between them
       uint32_t k0[KW], k1[KW];
-      kv8_load_krow<DH>(k0, kp + g * DH, t);
-      kv8_load_krow<DH>(k1, kp + (g + 8) * DH, t);
+      kv8_load_krow<DH>(k0, kp, g, t);
+      kv8_load_krow<DH>(k1, kp, g + 8, t);
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
         const uint2 x = kv8_half4<FMT>(k0[i]), y = kv8_half4<FMT>(k1[i]);
@@ -346,7 +365,11 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int p = QP - 1; p >= 0; --p) mma16816_f16(sc[u][n], f, qf[n][i][0][p], qf[n][i][1][p]);
+          for (int p = QP - 1; p >= 0; --p) mma16816_f16(NQ == 1 && (i & 1) ? odd : sc[u][n], f, qf[n][i][0][p], qf[n][i][1][p]);
+      }
+      if constexpr (NQ == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[u][0][e] += odd[e];
       }
       const float ks = kv8_pow2(meta.y & 0xff);
       const bool whole = pos[u] + kKv8Block <= minlim;
@@ -414,9 +437,9 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
         }
       }
       uint32_t v[4][VW];
-      const uint8_t* vp = sm.ring[warp][slot][u][1];
+      const uint8_t* vp = mine.ring[slot][u][1];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) kv8_load_vrow<DH>(v[r], vp + (2 * t + (r & 1) + (r >> 1) * 8) * DH, g);
+      for (int r = 0; r < 4; ++r) kv8_load_vrow<DH>(v[r], vp, 2 * t + (r & 1) + (r >> 1) * 8, g);
       if (pos[u] + kKv8Block > maxlim) {  // weight 0, but what lies there may be no number
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -450,7 +473,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     }
     cp_async_wait<0>();
   }
-  __syncthreads();  // the ring's memory takes the partial outputs
+  __syncwarp();  // the ring's memory takes the partial outputs
 
   // ---- join the warps
 #pragma unroll
@@ -462,11 +485,11 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int qn = n * 8 + 2 * t + e;
-      if (g == 0) sm.m[warp][qn] = m[n][e], sm.l[warp][qn] = x;
+      if (g == 0) mine.m[qn] = m[n][e], mine.l[qn] = x;
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        sm.o[warp][qn][kv8_vdim<DH>(2 * j, g)] = o[j][n][e] * vs;
-        sm.o[warp][qn][kv8_vdim<DH>(2 * j + 1, g)] = o[j][n][e + 2] * vs;
+        mine.o[qn][kv8_vdim<DH>(2 * j, g)] = o[j][n][e] * vs;
+        mine.o[qn][kv8_vdim<DH>(2 * j + 1, g)] = o[j][n][e + 2] * vs;
       }
     }
   __syncthreads();
@@ -477,17 +500,19 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     kv8_st4(a.out, DT, at, a.out_vec, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     if (d == 0 && a.lse) a.lse[(size_t)row_of(qn) * a.Hq + head_of(qn)] = L == 0.f ? -INFINITY : (M + log2f(L)) * ln2;
   };
-  for (int i = threadIdx.x; i < nq * (DH / 4); i += kKv8Warps * 32) {
+  for (int i = threadIdx.x; i < nq * (DH / 4); i += W * 32) {
     const int qn = i / (DH / 4), d = i % (DH / 4) * 4;
     float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kKv8Warps; ++w) M = fmaxf(M, sm.m[w][qn]);
+    for (int w = 0; w < kKv8Warps; ++w)
+      if (w < W) M = fmaxf(M, sm.w[w].m[qn]);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kKv8Warps; ++w) {
-      const float mw = sm.m[w][qn], f = mw == -INFINITY ? 0.f : ex2(mw - M);
-      const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][qn][d]);
-      L += f * sm.l[w][qn];
+      if (w >= W) break;
+      const float mw = sm.w[w].m[qn], f = mw == -INFINITY ? 0.f : ex2(mw - M);
+      const float4 x = *reinterpret_cast<const float4*>(&sm.w[w].o[qn][d]);
+      L += f * sm.w[w].l[qn];
       v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
     }
     if (CL == 1) {
@@ -502,7 +527,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
-  for (int i = rank * kKv8Warps * 32 + threadIdx.x; i < nq * (DH / 4); i += CL * kKv8Warps * 32) {
+  for (int i = rank * W * 32 + threadIdx.x; i < nq * (DH / 4); i += CL * W * 32) {
     const int qn = i / (DH / 4), d = i % (DH / 4) * 4;
     float M = -INFINITY, L = 0.f;
     for (int r = 0; r < CL; ++r) M = fmaxf(M, *cl.map_shared_rank(&sm.bm[qn], r));
@@ -521,19 +546,27 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 template <int DH, int FMT, int QP, int PP, int NQ>
 cudaError_t kv8_attend_one(const Kv8View& c, const Kv8AttnArgs& a, int max_keys, int sm_count, cudaStream_t stream) {
   auto kern = k_kv8_attend<DH, FMT, QP, PP, NQ>;
-  constexpr int smem = sizeof(Kv8Smem<DH, NQ>);
   const int tpr = (a.G + 8 * NQ - 1) / (8 * NQ);
   const long long tiles = a.sel_pages ? (long long)a.max_rows * tpr : ((long long)a.max_rows * a.G + 8 * NQ - 1) / (8 * NQ);
+  const long long ctas = tiles * c.H * c.batch;
   long long keys = a.sel_pages ? (long long)a.n_select * c.PT : max_keys;
   keys = max(keys, 1ll);
-  // Split the key axis over a cluster while the CTAs do not fill the GPU and each keeps a step per warp.
+  // Split the key axis over a cluster while the CTAs do not fill the GPU and each keeps a step per warp (one byte at 8192
+  // keys, 16 heads: 38.5 us whole, 13 us in eighths), and where CTAs are long enough that their end is uneven (64 sequences
+  // of 4096 to 8192 keys, 8 heads: 158 us whole, 149 us in halves; 16 of 4096, 16 heads: 32 and 36 us).
   int cl = 1;
-  while (cl < 8 && tiles * c.H * c.batch * cl < sm_count && keys >= (long long)cl * 2 * kKv8Warps * kKv8Block) cl *= 2;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  while (cl < 8 && ((ctas * cl < sm_count && keys >= (long long)cl * 2 * kKv8Warps * kKv8Block) ||
+                    (ctas * cl < 8 * sm_count && keys >= (long long)cl * 6144)))
+    cl *= 2;
+  // Eight warps a CTA, or four where many short CTAs wait for one another's start (1024 CTAs of 1024 selected keys: 43 us
+  // with eight warps, 36 us with four; 16 x 16 CTAs of 4096 keys: 32 and 36 us).
+  const int warps = ctas * cl >= 4 * sm_count && keys <= 2048 ? kKv8Warps / 2 : kKv8Warps;
+  const int smem = (int)kv8_smem<DH, NQ>(warps);
+  const cudaError_t e = kv8_allow_smem<k_kv8_attend<DH, FMT, QP, PP, NQ>>((int)kv8_smem<DH, NQ>(kKv8Warps));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * cl), (unsigned)c.H, (unsigned)c.batch);
-  cfg.blockDim = dim3(kKv8Warps * 32);
+  cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

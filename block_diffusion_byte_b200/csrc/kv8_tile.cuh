@@ -566,7 +566,7 @@ cudaError_t kv8_tile_one(const Kv8View& c, const Kv8AttnArgs& a, long long tiles
   // Split the keys over a cluster while all its CTAs still run at once (two an SM) and each keeps 16 tiles.
   int cl = 1;
   while (cl < 8 && ctas * cl * 2 <= 2 * sm_count && max_keys >= cl * 2 * 16 * kKvtN) cl *= 2;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = kv8_allow_smem<k_kv8_tile<DH, FMT, QP, PP>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(ctas * cl));
