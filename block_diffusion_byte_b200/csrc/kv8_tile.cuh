@@ -47,7 +47,7 @@ struct KvtSmem {
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
   int4 meta[SLOTS];  // a tile's key exponent, value exponent, missing blocks (bits)
-  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH>()], p_full, o_done[kvt_bufs<DH>()];
+  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH>()], p_full[kvt_bufs<DH>()], o_done[kvt_bufs<DH>()];
   uint32_t tmem;
   int max_lim;
 };
@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     }
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(sm.s_full + i, 1);
+      mbar_init(sm.p_full + i, kKvtQ);  // one a buffer: a warp may be done with the next tile before another with this
       mbar_init(sm.o_done + i, 1);
     }
-    mbar_init(&sm.p_full, kKvtQ);
     sm.max_lim = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       l += (s0 + s1) * kv8_pow2(127 - shift);
       kvt_st_wait();
       kvt_before();
-      mbar_arrive(&sm.p_full);
+      mbar_arrive(sm.p_full + j % BUFS);
     }
     // ---- the CTA's own sums
     if (nt > 0 && ok && !kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     for (int j = 0; ok && j < nt; ++j) {
       // the next tile's scores run under this tile's weights; their columns held P of a tile whose product is done
       const int b = j + 1 - BUFS;
-      if ((b >= 0 && !kvt_wait(sm.o_done + b % BUFS, (b / BUFS) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(&sm.p_full, j & 1)) {
+      if ((b >= 0 && !kvt_wait(sm.o_done + b % BUFS, (b / BUFS) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(sm.p_full + j % BUFS, (j / BUFS) & 1)) {
         ok = false;
         break;
       }

@@ -252,6 +252,53 @@ def test_attend_many_rows(B, dt, D, H, G, rows_, ctx, mask):
     check(c, q, out, lse, off, lim, scale, dt)
 
 
+def dense(c, d, q, off, lim, scale, planes):
+    """Cache.attend and its bounds for all rows at once, in 64 bits on the GPU."""
+    kv = []
+    for name in ("k", "v"):
+        x = torch.from_numpy(decode(d.t[name].cpu().numpy(), d.t[name + "_exp"].cpu().numpy(), c.fmt)).cuda()
+        kv.append(x[torch.from_numpy(c.table).cuda().long()].transpose(1, 2).flatten(2, 3))  # [B, H, n, D]
+    outs, errs = [], []
+    for s in range(len(off) - 1):
+        n = max(lim[off[s]:off[s + 1]])
+        k, v = (x[s, :, :n] for x in kv)
+        qs = q[off[s]:off[s + 1]].double().unflatten(1, (c.H, -1))  # [R, H, G, D]
+        z = torch.einsum("rhgd,hnd->rhgn", qs, k) * scale
+        z = z.masked_fill(torch.arange(n, device="cuda") >= i32(lim[off[s]:off[s + 1]])[:, None, None, None], float("-inf"))
+        mag = abs(scale) * torch.einsum("rhgd,hnd->rhgn", qs.abs(), k.abs()).amax(-1)
+        zmax = z.masked_fill(z == float("-inf"), 0).abs().amax(-1)
+        dd = mag * ((c.D + 4) * 2.0 ** -23 + 2.0 ** -22) + 2.0 ** -22 * (1 + zmax)
+        dd = dd + 2.0 ** -39 * abs(scale) * qs.abs().amax(-1) * k.abs().sum(-1).amax(-1)[None, :, None]
+        w = torch.softmax(z, -1)
+        outs.append(torch.einsum("rhgn,hnd->rhgd", w, v).flatten(1, 2))
+        e = torch.einsum("rhgn,hnd->rhgd", w, v.abs()) * (2 * dd + (n / 4 + 64) * 2.0 ** -23 + 2.0 ** -planes)[..., None]
+        # the largest value scale: at most twice the largest magnitude over top, as a block's exponent is the least
+        errs.append((e + 2.0 ** -33 * n * 2 * v.abs().amax()).flatten(1, 2))
+    return torch.cat(outs), torch.cat(errs)
+
+
+@pytest.mark.parametrize("dt,D,H,G,rows_,ctx,batch", [("bf16", 64, 8, 1, 1024, 1024, 4), ("f32", 64, 4, 1, 512, 2100, 1), ("f16", 128, 2, 2, 640, 1500, 2),
+                                                      ("f32", 128, 2, 1, 300, 3000, 1), ("bf16", 96, 4, 2, 777, 1001, 2), ("bf16", 32, 16, 1, 900, 900, 2),
+                                                      ("f32", 64, 16, 1, 1024, 4096, 1), ("bf16", 128, 8, 1, 700, 700, 4)])
+def test_attend_prompts_that_fill_the_gpu(B, dt, D, H, G, rows_, ctx, batch):
+    """Many tiles of keys and many CTAs at once, twice: every row in its bounds, and the same bits again."""
+    rng = np.random.default_rng(D + rows_)
+    lens = [ctx - 37 * s for s in range(batch)]
+    n = [rows_ - 37 * s for s in range(batch)]
+    c, d = filled(B, rng, "int8" if D != 96 else "e4m3", H, 64, D, lens)
+    off = [0] + [int(x) for x in np.cumsum(n)]
+    lim = [int(x) for s in range(batch) for x in range(lens[s] - n[s] + 1, lens[s] + 1)]
+    q = torch.from_numpy(rng.normal(size=(off[-1], H * G, D)) * 2).to(DT[dt]).cuda()
+    want, err = dense(c, d, q, off, lim, D ** -0.5, PLANES[dt])
+    first = None
+    for _ in range(3):
+        out, _ = d.attend(q, off, lim, max(n), D ** -0.5)
+        assert bool((((out.double() - want).abs() <= err + (want.abs() + err) * torch.finfo(DT[dt]).eps / 2 + 2.0 ** -25)).all())
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    assert int(d.status) == 0
+
+
 @pytest.mark.parametrize("dt,rows_", [("bf16", 1), ("f32", 3), ("f16", 140), ("f32", 140)])
 def test_attend_loud_keys_and_scales(B, dt, rows_):
     """Scores far apart (one key takes all the weight), a negative scale and scale 0 (all keys alike)."""
