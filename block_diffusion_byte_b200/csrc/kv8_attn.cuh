@@ -19,6 +19,13 @@
 // the bytes in flight (two CTAs of eight warps, 8 KB each ahead: 128 KB an SM) cover the memory's latency.
 // Warps are joined in shared memory, and the CTAs that split a long key axis (a cluster) over distributed
 // shared memory, in a fixed order: no workspace, no second launch, no atomics.
+//
+// Bound by memory at long contexts: 64 sequences of 4096 to 8192 keys, 8 heads of 128, four query heads each, e4m3: 150 us,
+// 5.4 TB/s (0.82 of the measured copy rate); the rest is uneven ends and the dependent work of a warp's step (about 340
+// instructions for 16 keys).  By the chain of lookups at its start (row range, limit, page, exponents: about 4 us) when
+// short: 4 rows at 1028 keys, 16 heads of 64, fp32: 6.8 us; one row at 8192: 12.7 us.  Steps on the way, on the 64
+// sequences: codes as bf16 with the next step in registers, one CTA an SM 282 us; f16 and the ring 171 us; queries
+// loaded at once 164 us; pieces moved off shared banks 158 us; keys in halves 150 us.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -578,15 +585,17 @@ cudaError_t kv8_attend_one(const Kv8View& c, const Kv8AttnArgs& a, int max_keys,
   return cudaLaunchKernelEx(&cfg, kern, c, a, cl);
 }
 
-constexpr int kKv8TileRows = 96;
 template <int DH, int FMT>
 cudaError_t kv8_tile_dh(const Kv8View& c, const Kv8AttnArgs& a, long long tiles, int max_keys, int sm_count, cudaStream_t st);
 
 template <int DH, int FMT>
 cudaError_t kv8_attend_dh(const Kv8View& c, const Kv8AttnArgs& a, int max_keys, int sm_count, cudaStream_t st) {
-  // many rows: tiles of 128 queries on tcgen05
-  const long long tiles = ((long long)a.max_rows * a.G + 127) / 128;
-  if (!a.sel_pages && (long long)a.max_rows * a.G >= kKv8TileRows && tiles * c.H * c.batch <= INT_MAX / 8)
+  // Many rows against many keys: tiles of 128 queries on tcgen05.  Such a CTA takes longer to start and to end (20 us), and a
+  // tile of few rows is mostly idle.  Few-row kernel / tiles, us, 16 heads of 64, bf16: 64 rows at 8192 keys 27 / 32, 96
+  // rows 45 / 31; 256 rows at 1024 keys 16 / 21; 8 sequences of 4096 keys, 64 rows 68 / 58, 48 rows 53 / 62.  8 heads of
+  // 128, f16: 48 rows at 8192 keys 35 / 33, 64 rows 51 / 33; 256 rows at 1024 keys 24 / 28.
+  const long long queries = (long long)a.max_rows * a.G, tiles = (queries + 127) / 128;
+  if (!a.sel_pages && queries >= 64 && queries * max_keys >= 3 << 17 && tiles * c.H * c.batch <= INT_MAX / 8)
     return kv8_tile_dh<DH, FMT>(c, a, tiles, max_keys, sm_count, st);
   // queries a tile: 8, or 16 where a tile can hold more than 8
   const bool wide = (a.sel_pages ? a.G : (long long)a.max_rows * a.G) > 8;

@@ -13,8 +13,16 @@
 // two, relative to the largest scale of the tile; that scale joins the factor of the exponent's argument (keys) or the
 // weights (values), so no instruction is spent on scales outside the conversion.  O is corrected only when a row's
 // maximum has grown by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
-// Bound by the exponentials (one a weight on the 16-a-clock unit) and by issue slots: the products at DH 64 take half
-// that time.  Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
+// Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
+//
+// Bound by the weights' work: one exponential each on the 16-a-clock unit (512 clocks a tile) and, in a thread, the chain
+// score -> maximum -> exponential -> f16 -> tensor memory (about 1000 clocks a tile and CTA, two CTAs an SM); the
+// products take 350 clocks a tile (one f16 plane each) and never wait.  Four causal prompts of 2048, 16 heads of 64, bf16:
+// 100 us, 344 TFLOP/s; 1024 fp32 rows at 8192 keys (two planes of q and of the weights): 100 us, 322 TFLOP/s.  Steps on
+// the way (the two in turn): 128-key tiles, S and P in one place 195, 327 us; masked and whole tiles apart 123, 186;
+// 64-key tiles with the next tile's S under this one's weights 105, 146; bulk copies converted in place, a warp a tile,
+// three S tiles 95, 132 (with one barrier for the weights of all tiles, which was wrong; 100 with one a tile); keys split
+// over a cluster where tiles are few -, 100.
 #pragma once
 
 #include <cstddef>
@@ -32,10 +40,15 @@ constexpr float kKvtGrow = 6.f;                       // growth of the maximum (
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
 
 constexpr int kKvtN = 64;                             // keys a tile
-template <int DH>
-__host__ __device__ constexpr int kvt_slots() { return DH <= 64 ? 4 : 2; }  // tiles of operands in shared memory
-template <int DH>
-__host__ __device__ constexpr int kvt_bufs() { return DH <= 64 ? 3 : 2; }  // tiles of S in tensor memory (256 columns a CTA)
+// Tiles of operands in shared memory: four and two CTAs an SM, or one CTA where a tile takes 32 KB.
+template <int DH, int QP>
+__host__ __device__ constexpr int kvt_slots() { return DH > 64 && QP == 1 ? 5 : 4; }
+// The tensor cores cut each sum to fp32 instead of rounding it, so a long chain of products drifts (8e-6 of fp32 outputs
+// at 4096 keys).  fp32 rows end the chain after this many tiles and add it to a total with rounding (1e-6); 0: one chain.
+template <int QP>
+__host__ __device__ constexpr int kvt_fold() { return QP == 2 ? 8 : 0; }
+template <int DH, int QP>
+__host__ __device__ constexpr int kvt_bufs() { return DH <= 64 && kvt_fold<QP>() ? 2 : 3; }  // tiles of S in tensor memory
 template <int DH>
 __host__ __device__ constexpr int kvt_cols() { return DH <= 64 ? 64 : 128; }  // columns of O (whole swizzle atoms of V)
 
@@ -43,11 +56,11 @@ template <int DH, int QP>
 struct KvtSmem {
   static constexpr int HALVES = DH > 64 ? 2 : 1;  // swizzle atoms of 64 channels
   uint8_t q[QP][HALVES][kKvtQ * 128];
-  static constexpr int SLOTS = kvt_slots<DH>();
+  static constexpr int SLOTS = kvt_slots<DH, QP>();
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
   int4 meta[SLOTS];  // a tile's key exponent, value exponent, missing blocks (bits)
-  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH>()], p_full[kvt_bufs<DH>()], o_done[kvt_bufs<DH>()];
+  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
   uint32_t tmem;
   int max_lim;
 };
@@ -57,7 +70,7 @@ struct KvtSums {  // a CTA's sums, in place of the operands
   float2 ml[kKvtQ];
 };
 template <int DH, int QP>
-constexpr size_t kvt_smem() { return sizeof(KvtSmem<DH, QP>) + 1024; }
+__host__ __device__ constexpr size_t kvt_smem() { return sizeof(KvtSmem<DH, QP>) + 1024; }
 
 // ------------------------------------------------------------------------ primitives
 // Shared-memory operand of 128-byte rows with 128-byte swizzle, 8-row groups 1024 bytes apart.  `lead`: bytes between
@@ -113,6 +126,15 @@ __device__ __forceinline__ void kvt_ld_wait(float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // the values are read after the wait
 }
+__device__ __forceinline__ void kvt_ld16(uint32_t taddr, uint32_t (&r)[16]) {  // waited for
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void kvt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n" ::"r"(taddr),
@@ -151,8 +173,11 @@ __device__ __forceinline__ int kvt_swz(int row, int c) { return row * 128 + ((c 
 template <int DH, int FMT, int QP, int PP>
 __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 ? 2 : 1)
     k_kv8_tile(const __grid_constant__ Kv8View c, const __grid_constant__ Kv8AttnArgs a, const int n_tiles, const int CL) {
-  constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH>(), BUFS = kvt_bufs<DH>();
-  constexpr int COL_O = BUFS * N;  // tensor memory: tiles of S (P's planes in place, N / 2 columns each), O
+  constexpr int N = kKvtN, NV = kvt_cols<DH>(), NB = N / kKv8Block, SLOTS = kvt_slots<DH, QP>(), BUFS = kvt_bufs<DH, QP>();
+  constexpr int FOLD = kvt_fold<QP>();
+  // tensor memory: tiles of S (P's planes in place, N / 2 columns each), O, the total of the chains before
+  constexpr int COL_O = BUFS * N, COL_T = COL_O + NV, COLS = COL_T + (FOLD ? NV : 0) <= 256 ? 256 : 512;
+  static_assert(COLS == 256 || kvt_smem<DH, QP>() > 113 * 1024, "two CTAs share an SM's 512 columns");
   constexpr int DT = QP == 2 ? BLT_T_F32 : PP == 1 ? BLT_T_BF16 : BLT_T_F16;  // a.dtype
   extern __shared__ uint8_t kvt_raw[];
   KvtSmem<DH, QP>& sm = *reinterpret_cast<KvtSmem<DH, QP>*>((reinterpret_cast<uintptr_t>(kvt_raw) + 1023) & ~(uintptr_t)1023);
@@ -180,7 +205,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 7) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(256));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
   }
   int lim = 0;
@@ -298,22 +323,31 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       l *= f;
       f *= kv8_pow2(max(127 + vrun - vnew, 0));
       vrun = vnew;
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+      const bool fold = FOLD && j > 0 && j % max(FOLD, 1) == 0;  // this tile's product begins a chain
+      if (j > 0 && (fold || __any_sync(0xffffffffu, f != 1.f))) {
         if (!kvt_wait(sm.o_done + (j - 1) % BUFS, ((j - 1) / BUFS) & 1)) {
           ok = false;
           break;
         }
         kvt_after();
 #pragma unroll 1
-        for (int c0 = 0; c0 < DH; c0 += 32) {
-          float x[32];
-          kvt_ld32(lane_base + COL_O + c0, x);
-          kvt_ld_wait(x);
-          uint32_t w[2][16];
+        for (int c0 = 0; c0 < DH; c0 += 16) {
+          uint32_t x[16], y[16];
+          kvt_ld16(lane_base + COL_O + c0, x);
+          if (FOLD && j > FOLD) {
+            kvt_ld16(lane_base + COL_T + c0, y);
+            if (fold) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i >> 4][i & 15] = __float_as_uint(x[i] * f);
-          kvt_st16(lane_base + COL_O + c0, w[0]);
-          kvt_st16(lane_base + COL_O + c0 + 16, w[1]);
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              kvt_st16(lane_base + COL_T + c0, y);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+          kvt_st16(lane_base + (fold ? COL_T : COL_O) + c0, x);
         }
       }
       // weights, times 2^(kKvtShift + value exponent below the reference)
@@ -344,6 +378,14 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     // ---- the CTA's own sums
     if (nt > 0 && ok && !kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
     kvt_after();
+    auto total = [&](int c0, float (&v)[32]) {  // and the chains before
+      if (!FOLD || nt <= FOLD) return;
+      float y[32];
+      kvt_ld32(lane_base + COL_T + c0, y);
+      kvt_ld_wait(y);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += y[i];
+    };
     if (ok && CL == 1) {  // out = O / l
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // nothing visible: 0; NaN stays
       const float unit = inv * kv8_pow2(vrun - kKvtShift);
@@ -354,6 +396,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         if (nt > 0) {
           kvt_ld32(lane_base + COL_O + c0, v);
           kvt_ld_wait(v);
+          total(c0, v);
         }
         if (mine) {
 #pragma unroll
@@ -376,6 +419,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
           float v[32];
           kvt_ld32(lane_base + COL_O + c0, v);
           kvt_ld_wait(v);
+          total(c0, v);
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(&sums.o[threadIdx.x][c0 + i]) = make_float4(v[i] * unit, v[i + 1] * unit, v[i + 2] * unit, v[i + 3] * unit);
@@ -436,10 +480,9 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     int entry = entry_of(first);
     for (int j = first; j < nt; j += kKvtLoaders) {
       const int slot = j % SLOTS;
-      // The slot's last tile is done with.  This warp's last wait was for tile j - 3 - SLOTS; where the slot has had
-      // another tile since (fewer than four slots), that one first: a barrier tells only two phases apart.
-      if ((SLOTS <= kKvtLoaders && j >= 2 * SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS) & 1)) ||
-          (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1))) {
+      // The slot's last tile is done with.  (A barrier tells two phases apart, and this warp saw tile j - 3 - SLOTS done.)
+      static_assert(SLOTS > kKvtLoaders, "the slot's tile before last came no later than that");
+      if (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1)) {
         ok = false;
         break;
       }
@@ -509,11 +552,12 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       if (lead) {
         const uint64_t vj = vd + (uint32_t)slot * KSLOT;
         const uint32_t pa = tmem + buf * N;
+        const bool going = FOLD ? j % max(FOLD, 1) > 0 : j > 0;  // the chain goes on
 #pragma unroll
         for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
           for (int k0 = 0; k0 < N; k0 += 16)  // 16 keys: two 8-row groups of V
-            kvt_mma_ts(tmem + COL_O, pa + p * (N / 2) + k0 / 2, vj + k0 * 8, io, j > 0 || p < PP - 1 || k0 > 0);
+            kvt_mma_ts(tmem + COL_O, pa + p * (N / 2) + k0 / 2, vj + k0 * 8, io, going || p < PP - 1 || k0 > 0);
         kvt_commit(sm.o_done + buf);
         kvt_commit(sm.kv_empty + slot);
       }
@@ -525,7 +569,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
   const bool all_ok = __syncthreads_and(ok) != 0;
   if (warp == 7) {
     kvt_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(256));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(COLS));
   }
   if (!all_ok && threadIdx.x == 0 && c.status) set_status(c.status, kErrDevice);
   if (CL == 1) return;

@@ -55,7 +55,7 @@ typedef struct {
   int32_t page_tokens;  /* multiple of 16, at most 256 */
   int32_t n_pages;      /* pages in the pool */
   int32_t batch;        /* sequences: rows of page_table, at most 65535 */
-  int32_t max_pages;    /* page_table [batch][max_pages] (max_pages * page_tokens < 2^31) */
+  int32_t max_pages;    /* page_table [batch][max_pages] (max_pages * page_tokens < 2^30) */
   int32_t reserved;     /* 0 */
   uint8_t *k, *v;       /* codes: page p, head h, position t, channel c at p * page_stride + (h * page_tokens + t) * head_dim + c */
   uint8_t *k_exp, *v_exp; /* exponents: p * exp_stride + h * (page_tokens / 16) + t / 16 */
@@ -103,7 +103,7 @@ typedef struct {
   int32_t dtype; /* BLT_T_* of q and out */
   int32_t n_q_heads; /* a multiple of n_heads; query head h reads head h / (n_q_heads / n_heads) */
   int32_t n_rows, max_rows;
-  int32_t max_keys; /* expected largest row_limit: chooses the launch shape, never the result's meaning */
+  int32_t max_keys; /* expected largest row_limit: chooses the launch shape, and with it the order of the sums */
   float scale;      /* finite */
   int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
   const int32_t *row_offsets; /* [batch + 1] */

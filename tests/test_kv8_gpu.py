@@ -184,6 +184,11 @@ def test_missing_pages_and_bad_offsets_are_reported_and_skipped(B):
     want = c.attend(1, q[1].double().cpu().numpy(), 16, 0.2)[0]  # the keys whose page is there
     assert np.abs(out[1].cpu().numpy() - want).max() < 1e-4
     d.status.zero_()
+    big = q.repeat(100, 1, 1)
+    out, _ = d.attend(big, [0, 100, 200], [40] * 200, 100, 0.2, max_keys=1 << 14)  # many-row tiles
+    assert int(d.status) == B.BLT_ERR_DEVICE
+    assert np.abs(out[101::2].cpu().numpy() - want).max() < 1e-4
+    d.status.zero_()
     out, _ = d.attend(q, [0, 1, 99], [40, 16], 5, 0.2)  # the second sequence's end is cut to the array
     assert int(d.status) == B.BLT_ERR_DEVICE and bool((out != 7.0).all())
     d.status.zero_()
@@ -248,8 +253,9 @@ def test_attend_many_rows(B, dt, D, H, G, rows_, ctx, mask):
     lim += [9, 9]  # rows of no sequence
     q = torch.from_numpy(rng.normal(size=(off[-1] + 2, H * G, D))).to(DT[dt]).cuda()
     scale = D ** -0.5
-    out, lse = d.attend(q, off, lim, rows_, scale)
-    check(c, q, out, lse, off, lim, scale, dt)
+    for keys in (None, 4096, 1 << 20):  # the expected keys choose between few-row and many-row tiles, and how the keys are split
+        out, lse = d.attend(q, off, lim, rows_, scale, max_keys=keys)
+        check(c, q, out, lse, off, lim, scale, dt)
 
 
 def dense(c, d, q, off, lim, scale, planes):
@@ -307,8 +313,9 @@ def test_attend_loud_keys_and_scales(B, dt, rows_):
     q = torch.from_numpy(rng.normal(size=(rows_, 2, 64)) * 30).to(DT[dt]).cuda()
     lim = [350 - i for i in range(rows_)]
     for scale in (1.0, -0.7, 0.0):
-        out, lse = d.attend(q, [0, rows_], lim, rows_, scale)
-        check(c, q, out, lse, [0, rows_], lim, scale, dt)
+        for keys in (350, 1 << 20):
+            out, lse = d.attend(q, [0, rows_], lim, rows_, scale, max_keys=keys)
+            check(c, q, out, lse, [0, rows_], lim, scale, dt)
 
 
 @pytest.mark.parametrize("dt,rows_", [("bf16", 2), ("f32", 2), ("f16", 150), ("f32", 150)])
@@ -318,12 +325,12 @@ def test_attend_ignores_what_lies_behind_the_limit(B, dt, rows_):
     c, d = filled(B, rng, "e4m3", 1, 32, 64, [200], max_pages=9)
     q = torch.from_numpy(rng.normal(size=(rows_, 1, 64))).to(DT[dt]).cuda()
     lim = [171 + i % 30 for i in range(rows_)]
-    a, la = d.attend(q, [0, rows_], lim, rows_, 0.125)
+    a, la = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=1 << 14)
     for name in ("k", "v"):
         d.t[name][d.table[0, 6].long(), :, 8:] = 255
         d.t[name][d.table[0, 7:].long()] = 127
         d.t[name + "_exp"][d.table[0, 7:].long()] = 255
-    b, lb = d.attend(q, [0, rows_], lim, rows_, 0.125)
+    b, lb = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=1 << 14)
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
@@ -367,7 +374,7 @@ def test_offsets_beyond_32_bits(B, rows_):
     assert np.array_equal(k[used[:50]].cpu().numpy(), c.k[tab[0, :50]])
     q = torch.randn(rows_, 1, D, device="cuda")
     lim = [lens[0]] * rows_
-    out, lse = d.attend(q, [0, rows_], lim, rows_, 0.2)
+    out, lse = d.attend(q, [0, rows_], lim, rows_, 0.2, max_keys=1 << 14)
     check(c, q, out, lse, [0, rows_], lim, 0.2, "f32")
 
 
