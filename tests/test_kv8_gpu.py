@@ -500,3 +500,56 @@ def test_captured_calls_replay_beside_each_other(B):
             wpart, _ = d.attend(q, [0, 1, 2], lim, 1, 0.125, max_keys=400, sel=sel)
             torch.cuda.synchronize()
             assert torch.equal(full, want) and torch.equal(sp, sel[0]) and torch.equal(part, wpart)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f32", 64), ("f16", 128)])
+def test_prompts_on_two_streams_and_in_graphs(B, dt, D):
+    """Many-row calls that share the cache run beside each other (and share SMs' tensor memory), eager and replayed."""
+    rng = np.random.default_rng(34)
+    c, d = filled(B, rng, "int8", 4, 64, D, [700, 513])
+    off, lim = [0, 300, 500], [401 + i for i in range(300)] + [314 + i for i in range(200)]
+    qs = [torch.randn(500, 8, D, device="cuda").to(DT[dt]) for _ in range(2)]
+    want = [d.attend(q, off, lim, 300, 0.1, max_keys=4096)[0] for q in qs]
+    offs, lims = i32(off), i32(lim)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for q, out, st in zip(qs, outs, streams):
+            B.blt_kv8_attend(d.desc, B.kv8_attention(q, out, offs, lims, 300, 4096, 0.1), st.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graphs = []
+    for q, out, st in zip(qs, outs, streams):
+        out.zero_()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            B.blt_kv8_attend(d.desc, B.kv8_attention(q, out, offs, lims, 300, 4096, 0.1), torch.cuda.current_stream().cuda_stream)
+        graphs.append(g)
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert int(d.status) == 0
+
+
+def test_smallest_calls(B):
+    """One row, one key, one head; a page of 16; rows and keys at a page's and a block's border; no rows in any sequence."""
+    rng = np.random.default_rng(35)
+    for n in (1, 15, 16, 17, 32, 33):
+        c, d = filled(B, rng, "e4m3", 1, 16, 32, [n])
+        q = torch.randn(1, 1, 32, device="cuda")
+        out, lse = d.attend(q, [0, 1], [n], 1, 1.0)
+        check(c, q, out, lse, [0, 1], [n], 1.0, "f32")
+        sel = d.select(q, [0, 1], [n], 1, 1, 0, 1)
+        assert sel[0][0, 0].tolist() == [(n - 1) // 16] and int(sel[1][0, 0]) == 1
+        out, lse = d.attend(q, [0, 1], [n], 1, 1.0, sel=sel)
+        check(c, q, out, lse, [0, 1], [n], 1.0, "f32", [[[(n - 1) // 16]]])
+        out, lse = d.attend(q, [0, 0], [n], 1, 1.0)
+        assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+        before = {name: t.clone() for name, t in d.t.items()}
+        d.append(q, q, [0, 0], [0], 1)
+        assert all(torch.equal(t, before[name]) for name, t in d.t.items())
