@@ -25,7 +25,8 @@
  *     blt_kv8_last_error() gives this thread's last message.  Nothing is queued on an error.
  *   - Errors found on the device (a page number outside the pool, offsets or positions out of range)
  *     are skipped over and reported as BLT_ERR_DEVICE in *status, if that is given; the call's other
- *     work is done.
+ *     work is done.  So is a wait inside a kernel that ran out (about a second; none should): the
+ *     rows concerned are then not written.
  *   - Calls run on the device that holds the cache's keys, whichever is current.
  *   - Rows of a call: sequence s owns rows row_offsets[s] .. row_offsets[s + 1] - 1 (at most max_rows).
  *     Rows outside every sequence are left as they were.
