@@ -9,7 +9,8 @@
 //              too, taken MN-major), a few tiles deep.  The codes of a block of 16 positions are one bulk copy into the
 //              place of the operand, converted there;
 //   warp 7     one thread issues the products.
-// Two CTAs share an SM, so one's products run under the other's exponentials.  Codes are whole in f16 times a power of
+// Two CTAs share an SM (heads of up to 64; one where a tile's operands take 32 KB), so one's products run under the
+// other's exponentials.  Codes are whole in f16 times a power of
 // two, relative to the largest scale of the tile; that scale joins the factor of the exponent's argument (keys) or the
 // weights (values), so no instruction is spent on scales outside the conversion.  O is corrected only when a row's
 // maximum has grown by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
@@ -18,11 +19,11 @@
 // Bound by the weights' work: one exponential each on the 16-a-clock unit (512 clocks a tile) and, in a thread, the chain
 // score -> maximum -> exponential -> f16 -> tensor memory (about 1000 clocks a tile and CTA, two CTAs an SM); the
 // products take 350 clocks a tile (one f16 plane each) and never wait.  Four causal prompts of 2048, 16 heads of 64, bf16:
-// 100 us, 344 TFLOP/s; 1024 fp32 rows at 8192 keys (two planes of q and of the weights): 100 us, 322 TFLOP/s.  Steps on
+// 98 us, 351 TFLOP/s; 1024 fp32 rows at 8192 keys (two planes of q and of the weights): 105 us, 306 TFLOP/s.  Steps on
 // the way (the two in turn): 128-key tiles, S and P in one place 195, 327 us; masked and whole tiles apart 123, 186;
 // 64-key tiles with the next tile's S under this one's weights 105, 146; bulk copies converted in place, a warp a tile,
 // three S tiles 95, 132 (with one barrier for the weights of all tiles, which was wrong; 100 with one a tile); keys split
-// over a cluster where tiles are few -, 100.
+// over a cluster where tiles are few -, 100; fp32 sums in chains of 8 tiles -, 105.
 #pragma once
 
 #include <cstddef>
