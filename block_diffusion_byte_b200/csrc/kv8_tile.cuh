@@ -26,6 +26,7 @@
 // over a cluster where tiles are few -, 100; fp32 sums in chains of 8 tiles -, 105.
 #pragma once
 
+#include <cfloat>
 #include <cstddef>
 
 #include "kv8.cuh"
@@ -300,7 +301,9 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
       const int4 meta = sm.meta[slot];
       const int pos0 = (j0 + j) * N;
-      const float ks = kv8_pow2(meta.x) * qs;
+      // A zero query or zero keys take the product below fp32's range: kept above 0 (its scores are 0 either way), so that a
+      // masked score, -inf, times it stays -inf.
+      const float ks = fmaxf(kv8_pow2(meta.x) * qs, FLT_MIN);
       const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim) && meta.z == 0;
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) kvt_ld_wait(v[i]);

@@ -1,0 +1,58 @@
+"""Attention over the 8-bit KV cache where queries, keys or values are zero, tiny, or blocks of very different scale.
+
+Both kernels (few rows, many rows: chosen by max_keys) against the definition, within the bounds of Cache.attend, which are
+made of what a row sees.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from _kv8_ref import Cache
+from test_kv8_gpu import B, DT, Dev, check, table  # noqa: F401  (B: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+KEYS = (0, 1 << 20)  # expected keys: few-row tiles, many-row tiles (from 64 queries on)
+
+
+def stored(B, rng, fmt, PT, k, v):  # noqa: F811
+    """A cache that holds one sequence's fp32 rows k, v [n, H, D]."""
+    n, H, D = k.shape
+    tab, n_pages = table(rng, 1, -(-n // PT))
+    c = Cache(fmt, n_pages, H, PT, D, tab, rng)
+    d = Dev(B, c)
+    d.append(*(torch.from_numpy(x).to(torch.float32).cuda() for x in (k, v)), [0, n], [0], n)
+    for name, t in d.t.items():
+        setattr(c, name, t.cpu().numpy())
+    return c, d
+
+
+@pytest.mark.parametrize("dt,D,PT", [("f32", 64, 64), ("bf16", 64, 16), ("f16", 128, 64), ("bf16", 96, 32), ("f32", 32, 64), ("f32", 128, 16)])
+@pytest.mark.parametrize("quiet", ["zero", "start", "tiny"])
+@pytest.mark.parametrize("mask", ["causal", "ragged"])
+def test_zero_and_tiny_queries_and_keys(B, dt, D, PT, quiet, mask):  # noqa: F811
+    """Padding in front of a prompt and zeroed buffers: scores of 0 give the mean of the values, hidden keys nothing."""
+    rng = np.random.default_rng(D + PT)
+    n, R = 200, 130
+    k, v = rng.normal(size=(2, n, 2, D))
+    if quiet == "zero":
+        k[:] = 0.0
+    elif quiet == "start":
+        k[:70] = 0.0
+        v[:30] = 0.0
+        k[70:130] *= 1e-9
+    else:
+        k *= 1e-30
+    c, d = stored(B, rng, "int8" if D != 96 else "e4m3", PT, k, v)
+    q = rng.normal(size=(R + 1, 2, D)) * np.array([0.0, 1e-9, 1.0, 1e-30, 0.0])[np.arange(R + 1) % 5][:, None, None]
+    q = torch.from_numpy(q).to(torch.float32).to(DT[dt]).cuda()
+    lim = list(range(n - R + 1, n + 1)) if mask == "causal" else [int(x) for x in rng.integers(0, n + 1, R)]
+    if mask == "ragged":
+        lim[:7] = [0, 0, 1, 33, 63, 64, 65]
+    lim.append(9)
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, R], lim, R, D ** -0.5, max_keys=keys)
+        assert bool(torch.isfinite(out).all()) and not bool(torch.isnan(lse).any())
+        check(c, q, out, lse, [0, R], lim, D ** -0.5, dt)
+    assert int(d.status) == 0
