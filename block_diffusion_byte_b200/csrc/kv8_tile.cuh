@@ -10,9 +10,9 @@
 //              place of the operand, converted there;
 //   warp 7     one thread issues the products.
 // Two CTAs share an SM (heads of up to 64; one where a tile's operands take 32 KB), so one's products run under the
-// other's exponentials.  Codes are whole in f16 times a power of
-// two, relative to the largest scale of the tile; that scale joins the factor of the exponent's argument (keys) or the
-// weights (values), so no instruction is spent on scales outside the conversion.  O is corrected only when a row's
+// other's exponentials.  Keys' codes are exact in f16 and enter as they are; a block's scale joins the factor of its
+// scores, so a loud block takes nothing from its neighbours.  Values' codes are whole in f16 times a power of two, relative
+// to the largest scale of the tile, which joins the weights.  O is corrected only when a row's
 // maximum has grown by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
 // Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
 //
@@ -61,7 +61,7 @@ struct KvtSmem {
   static constexpr int SLOTS = kvt_slots<DH, QP>();
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
-  int4 meta[SLOTS];  // a tile's key exponent, value exponent, missing blocks (bits)
+  int4 meta[SLOTS];  // a tile's key exponents (a byte a block), value exponent, missing blocks (bits)
   uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
   uint32_t tmem;
   int max_lim;
@@ -301,9 +301,11 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
       const int4 meta = sm.meta[slot];
       const int pos0 = (j0 + j) * N;
-      // A zero query or zero keys take the product below fp32's range: kept above 0 (its scores are 0 either way), so that a
-      // masked score, -inf, times it stays -inf.
-      const float ks = fmaxf(kv8_pow2(meta.x) * qs, FLT_MIN);
+      // Scales of the blocks' scores.  A zero query or zero keys take them below fp32's range: kept above 0 (the scores are 0
+      // either way), so that a masked score, -inf, times it stays -inf; and finite, so that a score of 0 stays 0.
+      float ks[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) ks[b] = fminf(fmaxf(kv8_pow2(meta.x >> 8 * b & 255) * qs, FLT_MIN), FLT_MAX);
       const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim) && meta.z == 0;
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) kvt_ld_wait(v[i]);
@@ -312,11 +314,13 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         for (int i = 0; i < N; ++i)
           if (pos0 + i >= lim || (meta.z >> (i / kKv8Block) & 1)) v[i / 32][i % 32] = -INFINITY;
       }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float mxb[NB], mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], v[i / 32][i % 32]);
-      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      mx = mx == -INFINITY ? mx : mx * ks;
+      for (int b = 0; b < NB; ++b) mxb[b] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i) mxb[i / kKv8Block] = fmaxf(mxb[i / kKv8Block], v[i / 32][i % 32]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) mx = fmaxf(mx, mxb[b] * ks[b]);
       // correction: a maximum that has grown too far, or louder values
       float f = 1.f;
       if (mx > m + kKvtGrow || (m == -INFINITY && mx > m)) {
@@ -363,7 +367,8 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         uint32_t w[PP][16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float p0 = ex2(fmaf(v[i][e], ks, off)), p1 = ex2(fmaf(v[i][e + 1], ks, off));
+          const int b = (i * 32 + e) / kKv8Block;
+          const float p0 = ex2(fmaf(v[i][e], ks[b], off)), p1 = ex2(fmaf(v[i][e + 1], ks[b], off));
           s0 += p0;
           s1 += p1;
           uint32_t pl[PP];
@@ -510,11 +515,12 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         ok = false;
         break;
       }
-      const int kref = max(__reduce_max_sync(0xffffffffu, ke), kKv8LowExp), vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
+      const unsigned kes = __reduce_or_sync(0xffffffffu, there ? (unsigned)ke << 8 * lane : 0u);
+      const int vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
       const int rows = min(max_lim - (j0 + j) * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
       // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
-      if (lane == 0) sm.meta[slot] = make_int4(kref, vref, (int)(~held & ((1u << nb) - 1)), 0);
-      convert(sm.k[slot], kvt_pow2_f16x2(kref - ke), held, N);
+      if (lane == 0) sm.meta[slot] = make_int4((int)kes, vref, (int)(~held & ((1u << nb) - 1)), 0);
+      convert(sm.k[slot], kvt_pow2_f16x2(0), held, N);
       convert(sm.v[slot], kvt_pow2_f16x2(vref - ve), held, rows);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(sm.kv_full + slot);

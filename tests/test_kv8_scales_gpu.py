@@ -56,3 +56,28 @@ def test_zero_and_tiny_queries_and_keys(B, dt, D, PT, quiet, mask):  # noqa: F81
         assert bool(torch.isfinite(out).all()) and not bool(torch.isnan(lse).any())
         check(c, q, out, lse, [0, R], lim, D ** -0.5, dt)
     assert int(d.status) == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,power", [(64, 18), (64, 26), (128, 30), (32, 26), (96, 60)])
+@pytest.mark.parametrize("rows_", [3, 130])
+def test_a_loud_key_without_weight_changes_no_other(B, dt, fmt, D, power, rows_):  # noqa: F811
+    """A block of keys far louder than its neighbours whose scores are far below theirs: the result is the others'."""
+    rng = np.random.default_rng(D + power)
+    n = 100
+    k, v = rng.normal(size=(2, n, 1, D))
+    k[..., 0] = 0.0
+    k[32:48] = 0.0
+    k[32:48, :, 0] = -2.0 ** power
+    c, d = stored(B, rng, fmt, 16, k, v)
+    qn = rng.normal(size=(rows_, 1, D))
+    qn[..., 0] = 1.0 + np.abs(qn[..., 0])
+    q = torch.from_numpy(qn).to(DT[dt]).cuda()
+    lim = [int(x) for x in rng.integers(49, n + 1, rows_)]
+    others = [[[0, 1, 3, 4, 5, 6]]] * rows_
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+        assert bool(torch.isfinite(out).all()) and not bool(torch.isnan(lse).any())
+        check(c, q, out, lse, [0, rows_], lim, 0.125, dt, others)
+    assert int(d.status) == 0
