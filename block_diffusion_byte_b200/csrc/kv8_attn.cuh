@@ -12,7 +12,8 @@
 // Codes become f16: both formats are exact in it (int8: 1024 + 128 + c read off the byte, less 1152; e4m3: the
 // converter), and a two-plane f16 operand has 22 bits where bf16 has 16.  f16's range is met by powers of two:
 // each query is scaled so that its largest channel lies in [2^14, 2^15), and weights times their block's scale are
-// taken relative to the largest block scale so far (times 2^14).  What lies 2^38 below the largest is cut.
+// taken relative to the largest block scale that the query has seen so far (times 2^14).  What lies 2^38 below the largest
+// is cut.
 //
 // Each warp takes 16-key units of its own with its own running maximum and sum, and copies them (cp.async)
 // through a ring of its own in shared memory, kKv8Stages - 1 steps ahead: no barrier stands between the warps, and
@@ -335,11 +336,12 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   }
 
   float m[NQ][2], l[NQ][2], o[MT][NQ][4];
-  int vref = kKv8LowExp;  // the largest value exponent so far; outputs are in units of 2^(vref - 127 - 14)
+  int vref[NQ][2];  // the largest value exponent that the query has seen; its outputs are in units of 2^(vref - 127 - 14)
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n][0] = m[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.f;
+    vref[n][0] = vref[n][1] = kKv8LowExp;
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -349,13 +351,11 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
   auto compute = [&](int slot) {
     float sc[U][NQ][4];
     int pos[U], ve[U];
-    int vmax = vref;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int2 meta = mine.meta[slot][u];
       pos[u] = meta.x;
       ve[u] = meta.y >> 8;
-      vmax = max(vmax, ve[u]);
       const uint8_t* kp = mine.ring[slot][u][0];
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
           if (!whole && pos[u] + g + (e >> 1) * 8 >= lim[n][e & 1]) sc[u][n][e] = -INFINITY;
         }
     }
-    bool grow = vmax > vref;
+    bool grow = false;
     float mn[NQ][2];
+    int vn[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -400,11 +401,13 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
         mn[n][e] = x;
-        grow |= x > m[n][e];
+        int y = vref[n][e];
+#pragma unroll
+        for (int u = 0; u < U; ++u) y = max(y, pos[u] < lim[n][e] ? ve[u] : 0);
+        vn[n][e] = y;
+        grow |= x > m[n][e] || y > vref[n][e];
       }
     if (__any_sync(0xffffffffu, grow)) {
-      const float vf = kv8_pow2(max(127 + vref - vmax, 0));  // beyond 2^-126: nothing is left of the sums
-      vref = vmax;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float f[2];
@@ -413,7 +416,8 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
           f[e] = mn[n][e] > m[n][e] ? ex2(m[n][e] - mn[n][e]) : 1.f;  // -inf before the first visible key: 0
           m[n][e] = mn[n][e];
           l[n][e] *= f[e];
-          f[e] *= vf;
+          f[e] *= kv8_pow2(max(127 + vref[n][e] - vn[n][e], 0));  // beyond 2^-126: nothing is left of the sums
+          vref[n][e] = vn[n][e];
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j)
@@ -424,16 +428,17 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t pf[NQ][2][PP];
-      const float vs = kv8_pow2(max(141 + ve[u] - vref, 0));  // 2^(14 + ve - vref)
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float p[4];
+        float p[4], vs[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) vs[e] = kv8_pow2(min(max(141 + ve[u] - vref[n][e], 0), 141));  // 2^(14 + ve - vref); louder: not seen
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float mx = m[n][e & 1];
           p[e] = ex2(sc[u][n][e] - (mx == -INFINITY ? 0.f : mx));
           l[n][e & 1] += p[e];
-          p[e] *= vs;
+          p[e] *= vs[e & 1];
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float x = l[n][e];
-      const float vs = kv8_pow2(vref - 14);
+      const float vs = kv8_pow2(vref[n][e] - 14);
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int qn = n * 8 + 2 * t + e;

@@ -81,3 +81,31 @@ def test_a_loud_key_without_weight_changes_no_other(B, dt, fmt, D, power, rows_)
         assert bool(torch.isfinite(out).all()) and not bool(torch.isnan(lse).any())
         check(c, q, out, lse, [0, rows_], lim, 0.125, dt, others)
     assert int(d.status) == 0
+
+
+def unseen(B, dt, fmt, D, step, loud, rows_, keys):  # noqa: F811
+    """Each block of 16 positions is 2^step louder than the one before: a row's result is as exact as what it sees."""
+    rng = np.random.default_rng(D + step)
+    nb = min(6, 110 // step + 1)
+    n = 16 * nb
+    k, v = rng.normal(size=(2, n, 1, D))
+    x = k if loud == "k" else v
+    x *= 2.0 ** (step * (np.arange(n) // 16))[:, None, None]
+    c, d = stored(B, rng, fmt, 32, k, v)
+    q = torch.from_numpy(rng.normal(size=(rows_, 1, D))).to(DT[dt]).cuda()
+    lim = [int(x) for x in rng.integers(1, n + 1, rows_)]
+    lim[:6] = [16, n, 5, 17, 32, 0]
+    out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+    assert bool(torch.isfinite(out).all()) and not bool(torch.isnan(lse).any())
+    check(c, q, out, lse, [0, rows_], lim, 0.125, dt)
+    assert int(d.status) == 0
+
+
+SCALES = pytest.mark.parametrize("dt,fmt,D,step", [(dt, fmt, D, step) for dt in ("f32", "bf16") for fmt in ("int8", "e4m3")
+                                                   for D, step in ((64, 17), (64, 26), (64, 34), (128, 26), (32, 34), (96, 17))])
+
+
+@SCALES
+@pytest.mark.parametrize("rows_", [6, 12])
+def test_values_that_a_row_does_not_see_few_rows(B, dt, fmt, D, step, rows_):  # noqa: F811
+    unseen(B, dt, fmt, D, step, "v", rows_, 0)
