@@ -10,10 +10,10 @@
 //              place of the operand, converted there;
 //   warp 7     one thread issues the products.
 // Two CTAs share an SM (heads of up to 64; one where a tile's operands take 32 KB), so one's products run under the
-// other's exponentials.  Keys' codes are exact in f16 and enter as they are; a block's scale joins the factor of its
-// scores, so a loud block takes nothing from its neighbours.  Values' codes are whole in f16 times a power of two, relative
-// to the largest scale of the tile, which joins the weights.  O is corrected only when a row's
-// maximum has grown by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
+// other's exponentials.  Codes are exact in f16 and enter as they are.  A block's key scale joins the factor of its
+// scores, its value scale the weights, relative to the largest one that the row itself sees: a loud block takes nothing
+// from its neighbours' keys, nor anything from rows that do not see it.  O is corrected only when a row's maximum has grown
+// by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
 // Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
 //
 // Bound by the weights' work: one exponential each on the 16-a-clock unit (512 clocks a tile) and, in a thread, the chain
@@ -40,6 +40,8 @@ constexpr int kKvtLoaders = 3;                        // warps that convert, a t
 constexpr long long kKvtWaitClocks = 2000000000ll;    // about a second
 constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
+// Least power of two that a weight is taken times: in f16 a weight (at most 2^kKvtGrow) rounds to 0 then, and l still has it.
+constexpr int kKvtLeast = -40;
 
 constexpr int kKvtN = 64;                             // keys a tile
 // Tiles of operands in shared memory: four and two CTAs an SM, or one CTA where a tile takes 32 KB.
@@ -61,7 +63,7 @@ struct KvtSmem {
   static constexpr int SLOTS = kvt_slots<DH, QP>();
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
-  int4 meta[SLOTS];  // a tile's key exponents (a byte a block), value exponent, missing blocks (bits)
+  int4 meta[SLOTS];  // a tile's key exponents and value exponents (a byte a block), missing blocks (bits), largest value exponent
   uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
   uint32_t tmem;
   int max_lim;
@@ -144,6 +146,11 @@ __device__ __forceinline__ void kvt_st16(uint32_t taddr, const uint32_t (&r)[16]
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void kvt_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void kvt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // A whole warp waits for phase `parity` of a barrier; false for all its lanes once the time is up.  (The SM's clock, not
 // the global timer, whose reading takes as long as a product.)
@@ -156,16 +163,6 @@ __device__ __forceinline__ bool kvt_wait(uint64_t* b, unsigned parity) {
     if (__all_sync(0xffffffffu, done)) return true;
     if (__any_sync(0xffffffffu, clock64() - t0 > kKvtWaitClocks)) return false;
   }
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// 2^-k as two f16, k >= 0; 0 beyond f16's range.
-__device__ __forceinline__ uint32_t kvt_pow2_f16x2(int k) {
-  const uint32_t h = k <= 14 ? (uint32_t)(15 - k) << 10 : k <= 24 ? 1u << (24 - k) : 0u;
-  return h | h << 16;
 }
 // Chunk c (16 bytes, 8 f16) of a 128-byte row in the 128-byte swizzle.
 __device__ __forceinline__ int kvt_swz(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
@@ -327,7 +324,12 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         f = ex2(m - mx);
         m = mx;
       }
-      const int vnew = max(vrun, meta.y);
+      int vnew = max(vrun, whole ? meta.w : 0);
+      if (!whole) {  // the blocks that this row sees
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          if (pos0 + b * kKv8Block < lim && !(meta.z >> b & 1)) vnew = max(vnew, meta.y >> 8 * b & 255);
+      }
       l *= f;
       f *= kv8_pow2(max(127 + vrun - vnew, 0));
       vrun = vnew;
@@ -358,17 +360,18 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
           kvt_st16(lane_base + (fold ? COL_T : COL_O) + c0, x);
         }
       }
-      // weights, times 2^(kKvtShift + value exponent below the reference)
-      const int shift = max(kKvtShift + meta.y - vrun, -100);
-      const float off = (float)shift - (m == -INFINITY ? 0.f : m);
-      float s0 = 0.f, s1 = 0.f;
+      // weights, times 2^(kKvtShift + the block's value exponent below the row's reference)
+      const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int i = 0; i < N / 32; ++i) {
-        uint32_t w[PP][16];
+      for (int b = 0; b < NB; ++b) {
+        const int shift = min(max(kKvtShift + (meta.y >> 8 * b & 255) - vrun, kKvtLeast), kKvtShift);
+        const float off = (float)shift - base;
+        float s0 = 0.f, s1 = 0.f;
+        uint32_t w[PP][8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int b = (i * 32 + e) / kKv8Block;
-          const float p0 = ex2(fmaf(v[i][e], ks[b], off)), p1 = ex2(fmaf(v[i][e + 1], ks[b], off));
+        for (int e = 0; e < kKv8Block; e += 2) {
+          const int i = b * kKv8Block + e;
+          const float p0 = ex2(fmaf(v[i / 32][i % 32], ks[b], off)), p1 = ex2(fmaf(v[i / 32][i % 32 + 1], ks[b], off));
           s0 += p0;
           s1 += p1;
           uint32_t pl[PP];
@@ -376,10 +379,10 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
 #pragma unroll
           for (int p = 0; p < PP; ++p) w[p][e >> 1] = pl[p];
         }
+        l += (s0 + s1) * kv8_pow2(127 - shift);
 #pragma unroll
-        for (int p = 0; p < PP; ++p) kvt_st16(sp + p * (N / 2) + i * 16, w[p]);
+        for (int p = 0; p < PP; ++p) kvt_st8(sp + p * (N / 2) + b * 8, w[p]);
       }
-      l += (s0 + s1) * kv8_pow2(127 - shift);
       kvt_st_wait();
       kvt_before();
       mbar_arrive(sm.p_full + j % BUFS);
@@ -455,9 +458,8 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     auto raw_of = [&](uint8_t (*dst)[N * 128], int b) {
       return PARTS == 1 ? dst[0] + b * kKv8Block * DH : dst[b / BP] + N * 64 + b % BP * kKv8Block * DH;
     };
-    // The tile's codes as f16 times lane b's factor for block b.  Blocks that are not `held`, and rows from `rows` on
-    // (they may be no numbers), become 0.
-    auto convert = [&](uint8_t (*dst)[N * 128], uint32_t fac, unsigned held, int rows) {
+    // The tile's codes as f16.  Blocks that are not `held`, and rows from `rows` on (they may be no numbers), become 0.
+    auto convert = [&](uint8_t (*dst)[N * 128], unsigned held, int rows) {
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
         uint4 w[PCH];
@@ -475,13 +477,10 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
 #pragma unroll
         for (int i = 0; i < PCH; ++i) {
           const int pc = i * 32 + lane, key = h * (N / PARTS) + pc / CPR, ch = pc % CPR * 16;
-          const uint32_t f = __shfl_sync(0xffffffffu, fac, key / kKv8Block);
           const uint2 x0 = kv8_half4<FMT>(w[i].x), x1 = kv8_half4<FMT>(w[i].y), x2 = kv8_half4<FMT>(w[i].z), x3 = kv8_half4<FMT>(w[i].w);
           uint8_t* d = dst[ch / 64];
-          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8)) =
-              make_uint4(mul_f16x2(x0.x, f), mul_f16x2(x0.y, f), mul_f16x2(x1.x, f), mul_f16x2(x1.y, f));
-          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8 + 1)) =
-              make_uint4(mul_f16x2(x2.x, f), mul_f16x2(x2.y, f), mul_f16x2(x3.x, f), mul_f16x2(x3.y, f));
+          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+          *reinterpret_cast<uint4*>(d + kvt_swz(key, ch % 64 / 8 + 1)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
         }
         if (PARTS > 1) __syncwarp();
       }
@@ -516,12 +515,13 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         break;
       }
       const unsigned kes = __reduce_or_sync(0xffffffffu, there ? (unsigned)ke << 8 * lane : 0u);
-      const int vref = max(__reduce_max_sync(0xffffffffu, ve), kKv8LowExp);
+      const unsigned ves = __reduce_or_sync(0xffffffffu, there ? (unsigned)ve << 8 * lane : 0u);
+      const int vmax = __reduce_max_sync(0xffffffffu, ve);
       const int rows = min(max_lim - (j0 + j) * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
       // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
-      if (lane == 0) sm.meta[slot] = make_int4((int)kes, vref, (int)(~held & ((1u << nb) - 1)), 0);
-      convert(sm.k[slot], kvt_pow2_f16x2(0), held, N);
-      convert(sm.v[slot], kvt_pow2_f16x2(vref - ve), held, rows);
+      if (lane == 0) sm.meta[slot] = make_int4((int)kes, (int)ves, (int)(~held & ((1u << nb) - 1)), vmax);
+      convert(sm.k[slot], held, N);
+      convert(sm.v[slot], held, rows);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(sm.kv_full + slot);
     }

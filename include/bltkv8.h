@@ -120,10 +120,12 @@ typedef struct {
 
 /* out = softmax(scale q K^T) V over each row's visible keys; a row that sees no key gets out 0 and
  * lse -inf.  Sums, maxima and products accumulate in fp32; fp32 q is used to 22 bits, and weights
- * enter the value product with 22 (F32, F16) or 11 (BF16) bits; channels and weights 2^32 below the
- * row's largest are cut.  Positions below row_limit have to be stored.  The same call gives the same bits;
- * the order of the sums, and with it the last bits, depends on max_rows, max_keys, batch and the
- * limits of the rows that share a tile.  n_rows = 0 or max_rows = 0: nothing is done.
+ * enter the value product with 22 (F32, F16) or 11 (BF16) bits.  Cut are channels of q 2^32 below the
+ * row's largest, and weights times their block's value scale 2^32 below the largest value scale among
+ * the blocks that the row sees; keys and values that a row does not see take nothing from it.
+ * Positions below row_limit have to be stored.  The same call gives the same bits; the order of the
+ * sums, and with it the last bits, depends on max_rows, max_keys, batch and the limits of the rows
+ * that share a tile.  n_rows = 0 or max_rows = 0: nothing is done.
  * Errors: INVALID_ARG, CUDA. */
 int blt_kv8_attend(const blt_kv8_cache *c, const blt_kv8_attention *a, void *stream);
 

@@ -109,3 +109,8 @@ SCALES = pytest.mark.parametrize("dt,fmt,D,step", [(dt, fmt, D, step) for dt in 
 @pytest.mark.parametrize("rows_", [6, 12])
 def test_values_that_a_row_does_not_see_few_rows(B, dt, fmt, D, step, rows_):  # noqa: F811
     unseen(B, dt, fmt, D, step, "v", rows_, 0)
+
+
+@SCALES
+def test_values_that_a_row_does_not_see_many_rows(B, dt, fmt, D, step):  # noqa: F811
+    unseen(B, dt, fmt, D, step, "v", 130, 1 << 20)
