@@ -38,6 +38,7 @@ constexpr int kKvtQ = 128;                            // queries a tile (tensor 
 constexpr int kKvtThreads = 256;                      // 16 warps of two CTAs leave 128 registers a thread
 constexpr int kKvtLoaders = 3;                        // warps that convert, a tile each in turn
 constexpr long long kKvtWaitClocks = 2000000000ll;    // about a second
+constexpr float kKvtLargeScore = 1048576.f;           // 2^20 (log 2): half a step of fp32 is 2^-4 there
 constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
 // Least power of two that a weight is taken times: in f16 a weight (at most 2^kKvtGrow) rounds to 0 then, and l still has it.
@@ -63,7 +64,7 @@ struct KvtSmem {
   static constexpr int SLOTS = kvt_slots<DH, QP>();
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
-  int4 meta[SLOTS];  // a tile's key exponents and value exponents (a byte a block), missing blocks (bits), largest value exponent
+  int4 meta[SLOTS];  // a tile's key exponents and value exponents (a byte a block), missing blocks (bits), largest key << 8 | value exponent
   uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
   uint32_t tmem;
   int max_lim;
@@ -303,13 +304,32 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       float ks[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) ks[b] = fminf(fmaxf(kv8_pow2(meta.x >> 8 * b & 255) * qs, FLT_MIN), FLT_MAX);
-      const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim) && meta.z == 0;
+      // A product is at most DH 2^15 top: no score of the tile is above kKvtLargeScore
+      const bool small = kv8_pow2(meta.w >> 8) * qs <= kKvtLargeScore / (DH * 32768.f * (FMT == 0 ? 128.f : 512.f));
+      const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim && meta.z == 0 && small);
+      float ref = 0.f;  // what the scores and m have been lessened by
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) kvt_ld_wait(v[i]);
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
           if (pos0 + i >= lim || (meta.z >> (i / kKv8Block) & 1)) v[i / 32][i % 32] = -INFINITY;
+        if (__any_sync(0xffffffffu, !small)) {
+          // Large scores: the fused products below are not rounded, and could exceed the rounded maximum by more than a
+          // weight has room for.  Round the scores here and take them relative to the maximum that comes out, in the
+          // products' own units, so that the rest stays as it is.
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < N; ++i) top = fmaxf(top, __fmul_rn(v[i / 32][i % 32], ks[i / kKv8Block]));
+          ref = top > m + kKvtGrow || m == -INFINITY ? top : m;
+          ref = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float k = ks[i / kKv8Block];
+            v[i / 32][i % 32] = (__fmul_rn(v[i / 32][i % 32], k) - ref) * (1.f / k);
+          }
+          m -= ref;
+        }
       }
       float mxb[NB], mx = -INFINITY;
 #pragma unroll
@@ -324,7 +344,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         f = ex2(m - mx);
         m = mx;
       }
-      int vnew = max(vrun, whole ? meta.w : 0);
+      int vnew = max(vrun, whole ? meta.w & 255 : 0);
       if (!whole) {  // the blocks that this row sees
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -383,6 +403,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
 #pragma unroll
         for (int p = 0; p < PP; ++p) kvt_st8(sp + p * (N / 2) + b * 8, w[p]);
       }
+      m += ref;
       kvt_st_wait();
       kvt_before();
       mbar_arrive(sm.p_full + j % BUFS);
@@ -516,10 +537,10 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       }
       const unsigned kes = __reduce_or_sync(0xffffffffu, there ? (unsigned)ke << 8 * lane : 0u);
       const unsigned ves = __reduce_or_sync(0xffffffffu, there ? (unsigned)ve << 8 * lane : 0u);
-      const int vmax = __reduce_max_sync(0xffffffffu, ve);
+      const int kmax = max(__reduce_max_sync(0xffffffffu, ke), 0), vmax = max(__reduce_max_sync(0xffffffffu, ve), 0);
       const int rows = min(max_lim - (j0 + j) * N, N), nb = (rows + kKv8Block - 1) / kKv8Block;
       // blocks before the end of the keys that have no page (blocks behind it are masked by the limits)
-      if (lane == 0) sm.meta[slot] = make_int4((int)kes, (int)ves, (int)(~held & ((1u << nb) - 1)), vmax);
+      if (lane == 0) sm.meta[slot] = make_int4((int)kes, (int)ves, (int)(~held & ((1u << nb) - 1)), kmax << 8 | vmax);
       convert(sm.k[slot], held, N);
       convert(sm.v[slot], held, rows);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");

@@ -114,3 +114,60 @@ def test_values_that_a_row_does_not_see_few_rows(B, dt, fmt, D, step, rows_):  #
 @SCALES
 def test_values_that_a_row_does_not_see_many_rows(B, dt, fmt, D, step):  # noqa: F811
     unseen(B, dt, fmt, D, step, "v", 130, 1 << 20)
+
+
+@SCALES
+@pytest.mark.parametrize("rows_,keys", [(12, 0), (130, 1 << 20)])
+def test_keys_that_a_row_does_not_see(B, dt, fmt, D, step, rows_, keys):  # noqa: F811
+    unseen(B, dt, fmt, D, step, "k", rows_, keys)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("D,power", [(64, 17), (64, 20), (96, 23), (64, 26), (64, 40), (128, 60), (32, 90), (96, 29)])
+@pytest.mark.parametrize("rows_", [3, 130])
+def test_scores_beyond_whole_numbers_of_fp32(B, dt, D, power, rows_):  # noqa: F811
+    """Scores around 2^power: where the largest leads by more than fp32's rounding of it, the row takes that key's value."""
+    rng = np.random.default_rng(D + power)
+    n = 180
+    k, v = rng.normal(size=(2, n, 1, D))
+    v[::3] *= 64.0
+    c, d = stored(B, rng, "int8", 32, k * 2.0 ** power, v)
+    q = torch.from_numpy(rng.normal(size=(rows_, 1, D))).to(DT[dt]).cuda()
+    lim = [int(x) for x in rng.integers(1, n + 1, rows_)]
+    keys_, values = (x[0] for x in c.keys(0, range(6)))
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+        for r in range(rows_):
+            qr = q[r, 0].double().cpu().numpy()
+            z = 0.125 * keys_[:lim[r]] @ qr
+            # a score's rounding: D + 4 steps of 2^-23 of the sum of magnitudes, and 2^-22 of q
+            err = 0.125 * (np.abs(keys_[:lim[r]]) @ np.abs(qr)).max() * ((D + 4) * 2.0 ** -23 + 2.0 ** -22)
+            first, second = np.sort(z)[::-1][:2] if lim[r] > 1 else (z[0], -np.inf)
+            assert abs(float(lse[r, 0]) - first) <= err + 2.0 ** -22 * abs(first) + np.log(n)
+            want = values[int(z.argmax())]
+            got = out[r, 0].double().cpu().numpy()
+            assert np.isfinite(got).all() and (np.abs(got) <= np.abs(values).max() * (1 + 2.0 ** -7)).all()
+            if first - second > 2 * err + 200:
+                assert (np.abs(got - want) <= np.abs(want) * torch.finfo(DT[dt]).eps / 2 + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [0, 22, 27, 60])
+@pytest.mark.parametrize("rows_", [3, 130])
+def test_equal_scores_of_any_size_give_the_mean(B, dt, power, rows_):  # noqa: F811
+    """The same key everywhere, values whose blocks differ in scale: the mean of what a row sees, whatever the score."""
+    rng = np.random.default_rng(power)
+    n, D = 100, 64
+    k, v = np.ones((n, 1, D)) * 2.0 ** power, rng.normal(size=(n, 1, D)) * 2.0 ** (np.arange(n) // 16)[:, None, None]
+    c, d = stored(B, rng, "int8", 32, k, v)
+    q = torch.full((rows_, 1, D), 1.25, dtype=DT[dt], device="cuda")
+    lim = [1 + (7 * i) % n for i in range(rows_)]
+    values = c.keys(0, range(4))[1][0]
+    for keys in KEYS:
+        out, _ = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+        for r in range(rows_):
+            seen = values[:lim[r]]
+            # weights are equal and exact; n + 64 roundings of sums of |v| / n, and the output's
+            tol = np.abs(seen).mean(0) * (n + 64) * 2.0 ** -23
+            want = seen.mean(0)
+            assert (np.abs(out[r, 0].double().cpu().numpy() - want) <= tol + (np.abs(want) + tol) * torch.finfo(DT[dt]).eps / 2).all()
