@@ -36,6 +36,7 @@ BLT_UNMASK_CONFIDENCE = 0
 BLT_UNMASK_EB = 1
 BLT_KV8_INT8 = 0
 BLT_KV8_E4M3 = 1
+BLT_KV8_TEST_STALL = 1  # test only: waits of blt_kv8_attend run out
 BLT_T_F32 = 0
 BLT_T_BF16 = 1
 BLT_T_F16 = 2
@@ -198,7 +199,7 @@ class blt_kv8_attention(C.Structure):
         ("sel_pages", C.c_void_p),
         ("sel_count", C.c_void_p),
         ("n_select", C.c_int32),
-        ("reserved", C.c_int32),
+        ("flags", C.c_int32),
     ]
 
 

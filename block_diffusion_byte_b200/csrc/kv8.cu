@@ -641,6 +641,7 @@ int blt_kv8_attend(const blt_kv8_cache* c, const blt_kv8_attention* t, void* str
   if ((t->sel_pages != nullptr) != (t->sel_count != nullptr)) return bad(BLT_ERR_INVALID_ARG, "sel_pages and sel_count come together");
   if (t->sel_pages && (t->n_select < 1 || (long long)t->n_select * c->page_tokens >= (1ll << 30)))
     return bad(BLT_ERR_INVALID_ARG, "n_select %d", t->n_select);
+  if (t->flags & ~BLT_KV8_TEST_STALL) return bad(BLT_ERR_INVALID_ARG, "flags %d", t->flags);
   if ((long long)max_rows * t->n_q_heads >= (1ll << 26)) return bad(BLT_ERR_INVALID_ARG, "%d rows of %d heads", max_rows, t->n_q_heads);
   DeviceScope dev;
   if (int rc = dev.enter(c->k)) return rc;
@@ -650,6 +651,7 @@ int blt_kv8_attend(const blt_kv8_cache* c, const blt_kv8_attention* t, void* str
   a.qs = t->q_row_stride, a.qhs = t->q_head_stride, a.os = t->out_row_stride, a.ohs = t->out_head_stride;
   a.row_off = t->row_offsets, a.row_limit = t->row_limit;
   a.sel_pages = t->sel_pages, a.sel_count = t->sel_count, a.n_select = t->n_select;
+  a.stall = (t->flags & BLT_KV8_TEST_STALL) != 0;
   a.q_vec = !misaligned(t->q, 16) && t->q_row_stride * es % 16 == 0 && t->q_head_stride * es % 16 == 0;
   a.out_vec = !misaligned(t->out, 16) && t->out_row_stride * es % 16 == 0 && t->out_head_stride * es % 16 == 0;
   const cudaError_t e = kv8_attend_launch(c->format, c->head_dim, v, a, t->max_keys, (cudaStream_t)stream);

@@ -231,6 +231,7 @@ struct Kv8AttnArgs {
   const int *sel_pages, *sel_count;
   int n_select;
   int q_vec, out_vec;  // rows of q (out) allow 16-byte loads (stores)
+  int stall;           // BLT_KV8_TEST_STALL
 };
 // Allows a kernel `bytes` of dynamic shared memory on the current device: asked of the driver once a device.
 template <auto KERN>

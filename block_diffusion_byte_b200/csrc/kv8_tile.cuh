@@ -14,7 +14,8 @@
 // scores, its value scale the weights, relative to the largest one that the row itself sees: a loud block takes nothing
 // from its neighbours' keys, nor anything from rows that do not see it.  O is corrected only when a row's maximum has grown
 // by more than 2^6 (weights carry 2^8 as room above f16's least) or a louder value scale comes.
-// Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word.
+// Every wait is bounded; one that runs out ends the CTA with BLT_ERR_DEVICE in the status word, and no CTA of its cluster
+// stores the tile's rows.
 //
 // Bound by the weights' work: one exponential each on the 16-a-clock unit (512 clocks a tile) and, in a thread, the chain
 // score -> maximum -> exponential -> f16 -> tensor memory (about 1000 clocks a tile and CTA, two CTAs an SM); the
@@ -38,6 +39,7 @@ constexpr int kKvtQ = 128;                            // queries a tile (tensor 
 constexpr int kKvtThreads = 256;                      // 16 warps of two CTAs leave 128 registers a thread
 constexpr int kKvtLoaders = 3;                        // warps that convert, a tile each in turn
 constexpr long long kKvtWaitClocks = 2000000000ll;    // about a second
+constexpr long long kKvtStallClocks = 20000000ll;     // where the waits are to run out
 constexpr float kKvtLargeScore = 1048576.f;           // 2^20 (log 2): half a step of fp32 is 2^-4 there
 constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
@@ -65,9 +67,9 @@ struct KvtSmem {
   uint8_t k[SLOTS][HALVES][kKvtN * 128];
   uint8_t v[SLOTS][HALVES][kKvtN * 128];
   int4 meta[SLOTS];  // a tile's key exponents and value exponents (a byte a block), missing blocks (bits), largest key << 8 | value exponent
-  uint64_t q_full, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
+  uint64_t q_full, drained, raw_full[SLOTS], kv_full[SLOTS], kv_empty[SLOTS], s_full[kvt_bufs<DH, QP>()], p_full[kvt_bufs<DH, QP>()], o_done[kvt_bufs<DH, QP>()];
   uint32_t tmem;
-  int max_lim;
+  int max_lim, ok;
 };
 template <int DH>
 struct KvtSums {  // a CTA's sums, in place of the operands
@@ -153,16 +155,16 @@ __device__ __forceinline__ void kvt_st8(uint32_t taddr, const uint32_t (&r)[8]) 
                : "memory");
 }
 __device__ __forceinline__ void kvt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// A whole warp waits for phase `parity` of a barrier; false for all its lanes once the time is up.  (The SM's clock, not
+// A whole warp waits for phase `parity` of a barrier; false for all its lanes once `clocks` are over.  (The SM's clock, not
 // the global timer, whose reading takes as long as a product.)
-__device__ __forceinline__ bool kvt_wait(uint64_t* b, unsigned parity) {
+__device__ __forceinline__ bool kvt_wait(uint64_t* b, unsigned parity, long long clocks) {
   bool done = mbar_try(b, parity);
   if (__all_sync(0xffffffffu, done)) return true;
   const long long t0 = clock64();
   while (true) {
     done = done || mbar_try(b, parity);
     if (__all_sync(0xffffffffu, done)) return true;
-    if (__any_sync(0xffffffffu, clock64() - t0 > kKvtWaitClocks)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > clocks)) return false;
   }
 }
 // Chunk c (16 bytes, 8 f16) of a 128-byte row in the 128-byte swizzle.
@@ -183,6 +185,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
   KvtSmem<DH, QP>& sm = *reinterpret_cast<KvtSmem<DH, QP>*>((reinterpret_cast<uintptr_t>(kvt_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % CL, item = blockIdx.x / CL;
+  auto wait = [&](uint64_t* b, unsigned parity) { return kvt_wait(b, parity, a.stall ? kKvtStallClocks : kKvtWaitClocks); };
   const int kvh = item % c.H, s = item / c.H % c.batch, tile = n_tiles - 1 - item / c.H / c.batch;
   int r0, r1;
   kv8_rows_of(a.row_off, s, a.n_rows, a.max_rows, c.status, r0, r1);
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.q_full, kKvtQ);
+    mbar_init(&sm.drained, 1);
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(sm.raw_full + i, 1);
       mbar_init(sm.kv_full + i, 32);
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     int vrun = kKv8LowExp;
     for (int j = 0; j < nt; ++j) {
       const int slot = j % SLOTS;
-      if (!kvt_wait(sm.s_full + j % BUFS, (j / BUFS) & 1) || !kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) {  // products, meta
+      if (!wait(sm.s_full + j % BUFS, (j / BUFS) & 1) || !wait(sm.kv_full + slot, (j / SLOTS) & 1)) {  // products, meta
         ok = false;
         break;
       }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       vrun = vnew;
       const bool fold = FOLD && j > 0 && j % max(FOLD, 1) == 0;  // this tile's product begins a chain
       if (j > 0 && (fold || __any_sync(0xffffffffu, f != 1.f))) {
-        if (!kvt_wait(sm.o_done + (j - 1) % BUFS, ((j - 1) / BUFS) & 1)) {
+        if (!wait(sm.o_done + (j - 1) % BUFS, ((j - 1) / BUFS) & 1)) {
           ok = false;
           break;
         }
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       mbar_arrive(sm.p_full + j % BUFS);
     }
     // ---- the CTA's own sums
-    if (nt > 0 && ok && !kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
+    if (nt > 0 && ok && !wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1)) ok = false;
     kvt_after();
     auto total = [&](int c0, float (&v)[32]) {  // and the chains before
       if (!FOLD || nt <= FOLD) return;
@@ -506,12 +510,13 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         if (PARTS > 1) __syncwarp();
       }
     };
+    const bool stall = a.stall && item == 0 && rank == 0 && first == 0;  // the tiles of this warp never come
     int entry = entry_of(first);
-    for (int j = first; j < nt; j += kKvtLoaders) {
+    for (int j = first; j < nt && !stall; j += kKvtLoaders) {
       const int slot = j % SLOTS;
       // The slot's last tile is done with.  (A barrier tells two phases apart, and this warp saw tile j - 3 - SLOTS done.)
       static_assert(SLOTS > kKvtLoaders, "the slot's tile before last came no later than that");
-      if (j >= SLOTS && !kvt_wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1)) {
+      if (j >= SLOTS && !wait(sm.kv_empty + slot, (j / SLOTS - 1) & 1)) {
         ok = false;
         break;
       }
@@ -531,8 +536,9 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
         ve = __ldg(c.ve + e);
       }
       entry = entry_of(j + kKvtLoaders);
-      if (!kvt_wait(sm.raw_full + slot, (j / SLOTS) & 1)) {
+      if (!wait(sm.raw_full + slot, (j / SLOTS) & 1)) {
         ok = false;
+        wait(sm.raw_full + slot, (j / SLOTS) & 1);  // the copies in flight
         break;
       }
       const unsigned kes = __reduce_or_sync(0xffffffffu, there ? (unsigned)ke << 8 * lane : 0u);
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     const uint64_t qd = kvt_desc(smem_u32(sm.q), 16), kd = kvt_desc(smem_u32(sm.k), 16), vd = kvt_desc(smem_u32(sm.v), N * 128);
     auto scores = [&](int j) {
       const int slot = j % SLOTS, buf = j % BUFS;
-      if (!kvt_wait(sm.kv_full + slot, (j / SLOTS) & 1)) return false;
+      if (!wait(sm.kv_full + slot, (j / SLOTS) & 1)) return false;
       kvt_after();
       if (lead) {
         const uint64_t kj = kd + (uint32_t)slot * KSLOT;
@@ -570,11 +576,11 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       __syncwarp();
       return true;
     };
-    ok = kvt_wait(&sm.q_full, 0) && scores(0);
+    ok = wait(&sm.q_full, 0) && scores(0);
     for (int j = 0; ok && j < nt; ++j) {
       // the next tile's scores run under this tile's weights; their columns held P of a tile whose product is done
       const int b = j + 1 - BUFS;
-      if ((b >= 0 && !kvt_wait(sm.o_done + b % BUFS, (b / BUFS) & 1)) || (j + 1 < nt && !scores(j + 1)) || !kvt_wait(sm.p_full + j % BUFS, (j / BUFS) & 1)) {
+      if ((b >= 0 && !wait(sm.o_done + b % BUFS, (b / BUFS) & 1)) || (j + 1 < nt && !scores(j + 1)) || !wait(sm.p_full + j % BUFS, (j / BUFS) & 1)) {
         ok = false;
         break;
       }
@@ -594,7 +600,13 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       }
       __syncwarp();
     }
-    if (ok) ok = kvt_wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1);  // nothing is in flight when the memory goes
+    // nothing is in flight when the memory goes
+    if (ok) ok = wait(sm.o_done + (nt - 1) % BUFS, ((nt - 1) / BUFS) & 1);
+    if (!ok) {
+      if (lead) kvt_commit(&sm.drained);
+      __syncwarp();
+      wait(&sm.drained, 0);
+    }
   }
   kvt_before();
   const bool all_ok = __syncthreads_and(ok) != 0;
@@ -602,14 +614,19 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     kvt_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(COLS));
   }
-  if (!all_ok && threadIdx.x == 0 && c.status) set_status(c.status, kErrDevice);
+  if (threadIdx.x == 0) {
+    if (!all_ok && c.status) set_status(c.status, kErrDevice);
+    sm.ok = all_ok;
+  }
   if (CL == 1) return;
   // ---- join the cluster and store: each CTA finishes a share of the rows, four channels a thread
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
+  bool every = true;  // no CTA's sums are missing
+  for (int r = 0; r < CL; ++r) every = every && *cl.map_shared_rank(&sm.ok, r);
   const int share = kKvtQ / CL;
-  for (int i = threadIdx.x; all_ok && i < share * (DH / 4); i += kKvtThreads) {
+  for (int i = threadIdx.x; every && i < share * (DH / 4); i += kKvtThreads) {
     const int qn = rank * share + i / (DH / 4), d = i % (DH / 4) * 4;
     if (qn >= nq) break;
     float M = -INFINITY, L = 0.f;

@@ -26,7 +26,7 @@
  *   - Errors found on the device (a page number outside the pool, offsets or positions out of range)
  *     are skipped over and reported as BLT_ERR_DEVICE in *status, if that is given; the call's other
  *     work is done.  So is a wait inside a kernel that ran out (about a second; none should): the
- *     rows concerned are then not written.
+ *     rows and heads concerned are then not written.
  *   - Calls run on the device that holds the cache's keys, whichever is current.
  *   - Rows of a call: sequence s owns rows row_offsets[s] .. row_offsets[s + 1] - 1 (at most max_rows).
  *     Rows outside every sequence are left as they were.
@@ -115,8 +115,11 @@ typedef struct {
    * than the one before it is ignored. */
   const int32_t *sel_pages, *sel_count;
   int32_t n_select;
-  int32_t reserved;
+  int32_t flags; /* 0 */
 } blt_kv8_attention;
+
+#define BLT_KV8_TEST_STALL 1 /* test only: in a call of many rows, the keys for the first sequence's last tile of 128
+                                queries and head 0 never come; waits run out within about 10 ms */
 
 /* out = softmax(scale q K^T) V over each row's visible keys; a row that sees no key gets out 0 and
  * lse -inf.  Sums, maxima and products accumulate in fp32; fp32 q is used to 22 bits, and weights
