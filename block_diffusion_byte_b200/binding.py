@@ -476,6 +476,8 @@ def kv8_cache(format, k, v, k_exp, v_exp, page_table, k_min=None, k_max=None, k_
     for t, name in ((k, "k"), (v, "v"), (k_exp, "k_exp"), (v_exp, "v_exp"), (k_min, "k_min"), (k_max, "k_max"), (k_sexp, "k_sexp")):
         if t is not None:
             _dense_from(t, name, 1)
+            if n > 1 and t.stride(0) == 0:  # 0 means dense to the library
+                raise ValueError(f"{name}: one page expanded over {n} (a page stride of 0)")
     for a, b, name in ((k, v, "k and v"), (k_exp, v_exp, "k_exp and v_exp"), (k_min, k_max, "k_min and k_max")):
         if a is not None and b is not None and n > 1 and a.stride(0) != b.stride(0):
             raise ValueError(f"{name}: page strides differ")

@@ -1,6 +1,7 @@
-"""Calls of the 8-bit KV cache that are refused, without a GPU: flags that mean nothing."""
+"""Calls of the 8-bit KV cache that are refused, without a GPU: flags that mean nothing, tensors that do not fit."""
 
 import pytest
+import torch
 
 from test_kv8 import B, _attn, _cache  # noqa: F401  (B: the fixture)
 
@@ -9,3 +10,42 @@ from test_kv8 import B, _attn, _cache  # noqa: F401  (B: the fixture)
 def test_unknown_flags_are_refused(B, flags):  # noqa: F811
     assert B.load_library().blt_kv8_attend(_cache(B), _attn(B, flags=flags), None) == B.BLT_ERR_INVALID_ARG
     assert b"flags" in B.load_library().blt_kv8_last_error()
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it lies on a GPU: the binding looks at tensors, it does not touch them."""
+
+    gpu = 0
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.gpu)
+
+
+class OnOtherGpu(OnGpu):
+    gpu = 1
+
+
+def gpu(*shape, dt=torch.uint8, on=OnGpu):
+    return torch.zeros(*shape, dtype=dt).as_subclass(on)
+
+
+def arrays(on=OnGpu, **kw):
+    i8 = torch.int8
+    return {**dict(k=gpu(4, 2, 32, 64, on=on), v=gpu(4, 2, 32, 64, on=on), k_exp=gpu(4, 2, 2, on=on), v_exp=gpu(4, 2, 2, on=on),
+                   page_table=gpu(1, 4, dt=torch.int32, on=on), k_min=gpu(4, 2, 64, dt=i8, on=on), k_max=gpu(4, 2, 64, dt=i8, on=on),
+                   k_sexp=gpu(4, 2, on=on)), **kw}
+
+
+@pytest.mark.parametrize("names", [("k", "v"), ("k_exp", "v_exp"), ("k_min", "k_max"), ("k_sexp",)])
+def test_one_page_expanded_over_the_pool_is_refused(B, names):  # noqa: F811
+    """A page stride of 0 means dense in the C struct: the kernels would go past the one page there is."""
+    a = arrays()
+    B.kv8_cache("int8", **a)
+    wrong = {n: a[n][:1].expand(a[n].shape) for n in names}
+    with pytest.raises(ValueError, match="expanded"):
+        B.kv8_cache("int8", **{**a, **wrong})
+    one = {n: t[:1] for n, t in arrays().items()}
+    one["page_table"] = gpu(1, 4, dt=torch.int32)
+    B.kv8_cache("int8", **one)  # a pool of one page
