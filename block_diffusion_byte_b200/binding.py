@@ -489,6 +489,7 @@ def kv8_cache(format, k, v, k_exp, v_exp, page_table, k_min=None, k_max=None, k_
                       _ptr(v_exp), stride(k), stride(k_exp), _ptr(k_min), _ptr(k_max), _ptr(k_sexp), stride(k_min), stride(k_sexp),
                       _ptr(page_table), _ptr(status))
     c.keep = (k, v, k_exp, v_exp, page_table, k_min, k_max, k_sexp, status)
+    c.device = dev
     return c
 
 
@@ -506,7 +507,7 @@ def kv8_rows(k, v, row_offsets, start, max_rows: int) -> blt_kv8_rows:
         raise ValueError(f"row_offsets has {row_offsets.shape[0]} entries for {start.shape[0]} sequences")
     r = blt_kv8_rows(_ptr(k), _ptr(v), _kv8_type(k), k.shape[0], int(max_rows), 0, k.stride(0), k.stride(1), _ptr(row_offsets), _ptr(start))
     r.keep = (k, v, row_offsets, start)
-    r.shape = (start.shape[0], k.shape[1], k.shape[2])
+    r.shape, r.device = (start.shape[0], k.shape[1], k.shape[2]), k.device
     return r
 
 
@@ -547,7 +548,7 @@ def kv8_attention(q, out, row_offsets, row_limit, max_rows: int, max_keys: int, 
                           q.stride(0), q.stride(1), out.stride(0), out.stride(1), _ptr(row_offsets), _ptr(row_limit), _ptr(sel_pages),
                           _ptr(sel_count), n_select, 0)
     a.keep = (q, out, row_offsets, row_limit, lse, sel_pages, sel_count)
-    a.shape = (row_offsets.shape[0] - 1, None if sel_pages is None else sel_pages.shape[1], q.shape[2])
+    a.shape, a.device = (row_offsets.shape[0] - 1, None if sel_pages is None else sel_pages.shape[1], q.shape[2]), q.device
     return a
 
 
@@ -559,7 +560,7 @@ def kv8_selection(q, row_offsets, row_limit, max_rows: int, max_keys: int, sel_p
     s = blt_kv8_selection(_ptr(q), _kv8_type(q), q.shape[1], q.shape[0], int(max_rows), int(max_keys), sel_pages.shape[2], int(n_sink),
                           int(n_local), q.stride(0), q.stride(1), _ptr(row_offsets), _ptr(row_limit), _ptr(sel_pages), _ptr(sel_count))
     s.keep = (q, row_offsets, row_limit, sel_pages, sel_count)
-    s.shape = (row_offsets.shape[0] - 1, sel_pages.shape[1], q.shape[2])
+    s.shape, s.device = (row_offsets.shape[0] - 1, sel_pages.shape[1], q.shape[2]), q.device
     return s
 
 
@@ -568,6 +569,8 @@ def _kv8_call(name: str, cache: blt_kv8_cache, args, stream) -> None:
         batch, heads, dim = args.shape
         if batch != cache.batch or dim != cache.head_dim or heads not in (None, cache.n_heads):
             raise ValueError(f"{name}: arguments for {batch} sequences, {heads} heads of {dim}; the cache has {cache.batch}, {cache.n_heads} of {cache.head_dim}")
+        if args.device != cache.device:
+            raise ValueError(f"{name}: arguments on {args.device}, the cache on {cache.device}")
         args.fits = cache
     rc = getattr(_lib or load_library(), name)(cache, args, stream)
     if rc != BLT_OK:

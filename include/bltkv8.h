@@ -27,7 +27,8 @@
  *     are skipped over and reported as BLT_ERR_DEVICE in *status, if that is given; the call's other
  *     work is done.  So is a wait inside a kernel that ran out (about a second; none should): the
  *     rows and heads concerned are then not written.
- *   - Calls run on the device that holds the cache's keys, whichever is current.
+ *   - Calls run on the device that holds the cache's keys, whichever is current; every other pointer
+ *     has to be one that this device may use, and `stream` one of its streams.
  *   - Rows of a call: sequence s owns rows row_offsets[s] .. row_offsets[s + 1] - 1 (at most max_rows).
  *     Rows outside every sequence are left as they were.
  */

@@ -49,3 +49,30 @@ def test_one_page_expanded_over_the_pool_is_refused(B, names):  # noqa: F811
     one = {n: t[:1] for n, t in arrays().items()}
     one["page_table"] = gpu(1, 4, dt=torch.int32)
     B.kv8_cache("int8", **one)  # a pool of one page
+
+
+def descriptors(B, on):  # noqa: F811
+    i32 = torch.int32
+    off, one, lim = gpu(2, dt=i32, on=on), gpu(1, dt=i32, on=on), gpu(3, dt=i32, on=on)
+    x, q = gpu(3, 2, 64, dt=torch.float32, on=on), gpu(3, 4, 64, dt=torch.float32, on=on)
+    sp, sc = gpu(3, 2, 4, dt=i32, on=on), gpu(3, 2, dt=i32, on=on)
+    rows = B.kv8_rows(x, x.clone(), off, one, 3)
+    return [("append", rows), ("read", rows), ("attend", B.kv8_attention(q, q.clone(), off, lim, 3, 64, 0.125)),
+            ("select", B.kv8_selection(q, off, lim, 3, 64, sp, sc))]
+
+
+@pytest.mark.parametrize("i", range(4))
+def test_arguments_on_another_device_than_the_cache_are_refused(B, i):  # noqa: F811
+    cache = B.kv8_cache("int8", **arrays())
+    name, args = descriptors(B, OnOtherGpu)[i]
+    with pytest.raises(ValueError, match="cuda:1"):
+        getattr(B, "blt_kv8_" + name)(cache, args)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the tensors only say that they lie on a GPU")
+@pytest.mark.parametrize("i", range(4))
+def test_arguments_on_the_same_device_reach_the_library(B, i):  # noqa: F811
+    cache = B.kv8_cache("int8", **arrays())
+    name, args = descriptors(B, OnGpu)[i]
+    with pytest.raises(B.BltError):  # no GPU here
+        getattr(B, "blt_kv8_" + name)(cache, args)
