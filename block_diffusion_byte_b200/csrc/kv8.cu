@@ -537,6 +537,20 @@ using namespace bltdec;
 
 namespace {
 
+// Queues a kernel.  The error is this launch's own: cudaGetLastError() could report what an earlier call of the thread left.
+template <class... P, class... A>
+int launch(const char* what, void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) return BLT_OK;
+  cudaGetLastError();
+  return cuda_bad(what, e);
+}
+
 struct AppendLaunch {
   const Kv8View& v;
   const Kv8RowsArgs& a;
@@ -545,10 +559,9 @@ struct AppendLaunch {
   cudaStream_t st;
   template <int DH, int FMT>
   int operator()() const {
-    if (a.dtype == BLT_T_F32) k_kv8_append<DH, FMT, BLT_T_F32><<<grid, threads, 0, st>>>(v, a);
-    else if (a.dtype == BLT_T_BF16) k_kv8_append<DH, FMT, BLT_T_BF16><<<grid, threads, 0, st>>>(v, a);
-    else k_kv8_append<DH, FMT, BLT_T_F16><<<grid, threads, 0, st>>>(v, a);
-    return 0;
+    auto go = [&](auto kern) { return launch("blt_kv8_append", kern, grid, threads, 0, st, v, a); };
+    return a.dtype == BLT_T_F32 ? go(k_kv8_append<DH, FMT, BLT_T_F32>)
+                                : a.dtype == BLT_T_BF16 ? go(k_kv8_append<DH, FMT, BLT_T_BF16>) : go(k_kv8_append<DH, FMT, BLT_T_F16>);
   }
 };
 struct ReadLaunch {
@@ -559,10 +572,9 @@ struct ReadLaunch {
   cudaStream_t st;
   template <int DH, int FMT>
   int operator()() const {
-    if (a.dtype == BLT_T_F32) k_kv8_read<DH, FMT, BLT_T_F32><<<grid, threads, 0, st>>>(v, a);
-    else if (a.dtype == BLT_T_BF16) k_kv8_read<DH, FMT, BLT_T_BF16><<<grid, threads, 0, st>>>(v, a);
-    else k_kv8_read<DH, FMT, BLT_T_F16><<<grid, threads, 0, st>>>(v, a);
-    return 0;
+    auto go = [&](auto kern) { return launch("blt_kv8_read", kern, grid, threads, 0, st, v, a); };
+    return a.dtype == BLT_T_F32 ? go(k_kv8_read<DH, FMT, BLT_T_F32>)
+                                : a.dtype == BLT_T_BF16 ? go(k_kv8_read<DH, FMT, BLT_T_BF16>) : go(k_kv8_read<DH, FMT, BLT_T_F16>);
   }
 };
 struct SelectLaunch {
@@ -575,16 +587,13 @@ struct SelectLaunch {
   template <int DH, int FMT>
   int operator()() const {
     const cudaError_t e = kv8_allow_smem<k_kv8_select<DH>>(kKv8MaxSelPages * 4 + 64 * (DH / 4 * 8 + 4));
-    if (e != cudaSuccess) return cuda_bad("blt_kv8_select", e);
-    k_kv8_select<DH><<<grid, threads, smem, st>>>(v, a);
-    return 0;
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_bad("blt_kv8_select", e);
+    }
+    return launch("blt_kv8_select", k_kv8_select<DH>, grid, threads, smem, st, v, a);
   }
 };
-
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? BLT_OK : cuda_bad(what, e);
-}
 
 int store_or_read(const blt_kv8_cache* c, const blt_kv8_rows* rows, void* stream, bool store) {
   g_err[0] = 0;
@@ -606,9 +615,8 @@ int store_or_read(const blt_kv8_cache* c, const blt_kv8_rows* rows, void* stream
   const int blocks = c->page_tokens / 16, touched = (a.max_rows + 30) / 16;
   int warps = 2 * (blocks < touched ? blocks : touched);
   warps = warps < 4 ? 4 : warps > kKv8RowThreads / 32 ? kKv8RowThreads / 32 : warps;
-  if (store) by_dim(c->head_dim, c->format, AppendLaunch{v, a, grid, warps * 32, (cudaStream_t)stream});
-  else by_dim(c->head_dim, c->format, ReadLaunch{v, a, grid, warps * 32, (cudaStream_t)stream});
-  return launched(store ? "blt_kv8_append" : "blt_kv8_read");
+  return store ? by_dim(c->head_dim, c->format, AppendLaunch{v, a, grid, warps * 32, (cudaStream_t)stream})
+               : by_dim(c->head_dim, c->format, ReadLaunch{v, a, grid, warps * 32, (cudaStream_t)stream});
 }
 
 }  // namespace
@@ -659,7 +667,7 @@ int blt_kv8_attend(const blt_kv8_cache* c, const blt_kv8_attention* t, void* str
     cudaGetLastError();
     return cuda_bad("blt_kv8_attend", e);
   }
-  return launched("blt_kv8_attend");
+  return BLT_OK;
 }
 
 int blt_kv8_select(const blt_kv8_cache* c, const blt_kv8_selection* t, void* stream) {
@@ -696,8 +704,7 @@ int blt_kv8_select(const blt_kv8_cache* c, const blt_kv8_selection* t, void* str
   // pages: 25 us with 512 threads)
   const int want = (t->max_keys + c->page_tokens - 1) / c->page_tokens;
   const int threads = want <= 128 ? 128 : want <= 256 ? 256 : kKv8SelThreads;
-  if (int rc = by_dim(c->head_dim, c->format, SelectLaunch{v, a, grid, threads, smem, (cudaStream_t)stream})) return rc;
-  return launched("blt_kv8_select");
+  return by_dim(c->head_dim, c->format, SelectLaunch{v, a, grid, threads, smem, (cudaStream_t)stream});
 }
 
 const char* blt_kv8_last_error(void) { return g_err; }
