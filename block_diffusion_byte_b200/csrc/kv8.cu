@@ -74,7 +74,11 @@ __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_c
           if (pos < start) {
             kv8_decode8<FMT>(*reinterpret_cast<const uint2*>(codes + gi * 8), x[j]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[j][e] *= old;
+            for (int e = 0; e < 8; ++e) {
+              // beyond fp32's range: an infinity where the code is the largest, else a number near the range's end
+              const float y = x[j][e] * old;
+              x[j][e] = fabsf(y) > FLT_MAX && fabsf(x[j][e]) < (FMT == 0 ? 127.f : 448.f) ? copysignf(FLT_MAX, y) : y;
+            }
           } else if (pos < end) {
             kv8_ld8(src, DT, (long long)(r0 + pos - start) * a.rs + (long long)h * a.hs + ch, a.vec, x[j]);
           } else {

@@ -12,7 +12,7 @@
  * exact in bf16.  A value is off by at most half a step: 2^(e - 128) for int8 (at most amax / 127),
  * 2^-4 of itself (or 2^(e - 137) where e4m3 is subnormal) for e4m3.  In a block with magnitudes near
  * fp32's largest a code's value can lie beyond it: it reads back as infinity and counts as fp32's
- * largest in a summary.
+ * largest in a summary and, if it was a number, when the block is quantised again.
  *
  * Conventions common to every call
  *   - The cache and its buffers belong to the caller; nothing is kept between calls, allocated, or

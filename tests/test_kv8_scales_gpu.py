@@ -171,3 +171,26 @@ def test_equal_scores_of_any_size_give_the_mean(B, dt, power, rows_):  # noqa: F
             tol = np.abs(seen).mean(0) * (n + 64) * 2.0 ** -23
             want = seen.mean(0)
             assert (np.abs(out[r, 0].double().cpu().numpy() - want) <= tol + (np.abs(want) + tol) * torch.finfo(DT[dt]).eps / 2).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("top", [float(np.finfo(np.float32).max), 3.39e38, 1e38, 1e-38])
+def test_kept_rows_near_the_ends_of_fp32(B, fmt, top):  # noqa: F811
+    """Rows stored one by one behind rows of magnitudes whose codes' values lie beyond fp32: the kept codes stay."""
+    c = Cache(fmt, 1, 1, 16, 32, [[0]], np.random.default_rng(0))
+    d = Dev(B, c)
+    x = torch.tensor([top, -top, top / 2, 1.0], device="cuda")[:, None, None].expand(4, 1, 32).contiguous()
+    loudest = 0
+    for i in range(4):
+        d.append(x[i:i + 1], x[i:i + 1], [0, 1], [i], 1)
+        e = int(d.t["k_exp"])
+        assert int(d.t["v_exp"]) == e and torch.equal(d.t["k"][0, 0, :i + 1], d.t["v"][0, 0, :i + 1])
+        loudest = max(loudest, e)
+        assert e == loudest  # the least exponent whose range holds every row: it does not fall
+        setattr(c, "k", d.t["k"].cpu().numpy())
+        setattr(c, "k_exp", d.t["k_exp"].cpu().numpy())
+        got = c.keys(0, [0])[0][0, :i + 1, 0]
+        want = x[:i + 1, 0, 0].double().cpu().numpy()
+        # off by at most one step of the largest exponent: 1 code, or 2^-3 of an e4m3 value (its subnormals: 2^-9)
+        step = 2.0 ** (loudest - 127) * (np.ones(i + 1) if fmt == "int8" else np.maximum(np.abs(want) / 2.0 ** (loudest - 127) * 2.0 ** -3, 2.0 ** -9))
+        assert (np.abs(got - want) <= step).all(), (i, got, want)
