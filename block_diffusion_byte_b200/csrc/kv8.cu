@@ -512,14 +512,14 @@ int by_dim(int dh, int fmt, F f) {
   return fmt == BLT_KV8_INT8 ? f.template operator()<128, 0>() : f.template operator()<128, 1>();
 }
 
-// Streaming multiprocessors of the current device (asked once per device; the same answer every time).
+// Streaming multiprocessors of the current device (asked once per device; the same answer every time, from any thread).
 int sm_count() {
-  static int known[64] = {};
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (dev < 64 && known[dev]) return known[dev];
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
-  if (dev < 64) known[dev] = n;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

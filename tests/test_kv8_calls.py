@@ -76,3 +76,21 @@ def test_arguments_on_the_same_device_reach_the_library(B, i):  # noqa: F811
     name, args = descriptors(B, OnGpu)[i]
     with pytest.raises(B.BltError):  # no GPU here
         getattr(B, "blt_kv8_" + name)(cache, args)
+
+
+def test_threads_have_messages_of_their_own(B):  # noqa: F811
+    import threading
+
+    lib, seen = B.load_library(), {}
+
+    def work(i):
+        for _ in range(200):
+            assert lib.blt_kv8_attend(_cache(B), _attn(B, dtype=10 + i), None) == B.BLT_ERR_INVALID_ARG
+            seen.setdefault(i, set()).add(lib.blt_kv8_last_error())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert seen == {i: {b"dtype %d" % (10 + i)} for i in range(8)}
