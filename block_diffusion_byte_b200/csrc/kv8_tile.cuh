@@ -655,9 +655,12 @@ cudaError_t kv8_tile_one(const Kv8View& c, const Kv8AttnArgs& a, long long tiles
   auto kern = k_kv8_tile<DH, FMT, QP, PP>;
   constexpr int smem = (int)kvt_smem<DH, QP>();
   const long long ctas = tiles * c.H * c.batch;
-  // Split the keys over a cluster while all its CTAs still run at once (two an SM) and each keeps 16 tiles.
+  // Split the keys over a cluster while all CTAs still run at once and each keeps 16 tiles.  Heads of 128, bf16, 8192 keys,
+  // one CTA an SM, us: 20 CTAs 59 in eighths (two waves), 45 in quarters; 64 CTAs 89 in quarters, 76 in halves; 128 CTAs 150
+  // in halves, 127 whole.  Of clusters of 8 with an SM a CTA, 12 run at once and 16 do not (59 us, 45 in quarters).
+  constexpr int per_sm = kvt_smem<DH, QP>() <= 113 * 1024 ? 2 : 1;
   int cl = 1;
-  while (cl < 8 && ctas * cl * 2 <= 2 * sm_count && max_keys >= cl * 2 * 16 * kKvtN) cl *= 2;
+  while (cl < 8 && ctas * cl * 2 <= (long long)per_sm * sm_count && (per_sm == 2 || cl < 4 || ctas <= 12) && max_keys >= cl * 2 * 16 * kKvtN) cl *= 2;
   const cudaError_t e = kv8_allow_smem<k_kv8_tile<DH, FMT, QP, PP>>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
