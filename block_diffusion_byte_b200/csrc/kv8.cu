@@ -504,6 +504,11 @@ int check_rows(const blt_kv8_cache* c, const blt_kv8_rows* r, Kv8RowsArgs& a) {
   return BLT_OK;
 }
 
+// Rows to be written that share elements with the next row or head.
+bool overlap(int rows, long long row_stride, int heads, long long head_stride, int dim) {
+  return (rows > 1 && row_stride < dim) || (heads > 1 && head_stride < dim);
+}
+
 template <class F>
 int by_dim(int dh, int fmt, F f) {
   if (dh == 32) return fmt == BLT_KV8_INT8 ? f.template operator()<32, 0>() : f.template operator()<32, 1>();
@@ -606,6 +611,7 @@ int store_or_read(const blt_kv8_cache* c, const blt_kv8_rows* rows, void* stream
   if (int rc = check_cache(c, v)) return rc;
   if (int rc = check_rows(c, rows, a)) return rc;
   if (a.max_rows == 0) return BLT_OK;
+  if (!store && overlap(a.n_rows, a.rs, c->n_heads, a.hs, c->head_dim)) return bad(BLT_ERR_INVALID_ARG, "rows to be written overlap");
   DeviceScope dev;
   if (int rc = dev.enter(c->k)) return rc;
   // rows at any position touch at most this many pages
@@ -650,6 +656,7 @@ int blt_kv8_attend(const blt_kv8_cache* c, const blt_kv8_attention* t, void* str
     return bad(BLT_ERR_INVALID_ARG, "a misaligned pointer in the attention");
   if (t->q_row_stride < 0 || t->q_head_stride < 0 || t->out_row_stride < 0 || t->out_head_stride < 0)
     return bad(BLT_ERR_INVALID_ARG, "a negative stride in the attention");
+  if (overlap(t->n_rows, t->out_row_stride, t->n_q_heads, t->out_head_stride, c->head_dim)) return bad(BLT_ERR_INVALID_ARG, "rows of out overlap");
   if ((t->sel_pages != nullptr) != (t->sel_count != nullptr)) return bad(BLT_ERR_INVALID_ARG, "sel_pages and sel_count come together");
   if (t->sel_pages && (t->n_select < 1 || (long long)t->n_select * c->page_tokens >= (1ll << 30)))
     return bad(BLT_ERR_INVALID_ARG, "n_select %d", t->n_select);

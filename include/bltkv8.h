@@ -95,12 +95,12 @@ typedef struct {
 int blt_kv8_append(const blt_kv8_cache *c, const blt_kv8_rows *rows, void *stream);
 
 /* The values at positions start[s] ..., written to rows (exact in BF16 and F32; rounded in F16).
- * Rows whose page is missing become 0. */
+ * Rows whose page is missing become 0.  Rows and heads must not share elements. */
 int blt_kv8_read(const blt_kv8_cache *c, const blt_kv8_rows *rows, void *stream);
 
 typedef struct {
   const void *q; /* row r, head h, channel c at r * q_row_stride + h * q_head_stride + c (elements) */
-  void *out;     /* the same with its own strides; same dtype; must not overlap q */
+  void *out;     /* the same with its own strides; same dtype; must not overlap q, nor a row or head another */
   float *lse;    /* [n_rows][n_q_heads] log-sum-exp (natural, of the scaled scores), or NULL */
   int32_t dtype; /* BLT_T_* of q and out */
   int32_t n_q_heads; /* a multiple of n_heads; query head h reads head h / (n_q_heads / n_heads) */

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from test_kv8 import B, _attn, _cache  # noqa: F401  (B: the fixture)
+from test_kv8 import B, _attn, _cache, _rows  # noqa: F401  (B: the fixture)
 
 
 @pytest.mark.parametrize("flags", [2, 3, -1, 1 << 30])
@@ -94,3 +94,19 @@ def test_threads_have_messages_of_their_own(B):  # noqa: F811
     for t in threads:
         t.join()
     assert seen == {i: {b"dtype %d" % (10 + i)} for i in range(8)}
+
+
+@pytest.mark.parametrize("kw", [dict(out_row_stride=0), dict(out_row_stride=32), dict(out_head_stride=0), dict(out_head_stride=63)],
+                         ids=lambda kw: ",".join(f"{k}={v}" for k, v in kw.items()))
+def test_rows_of_out_that_share_elements_are_refused(B, kw):  # noqa: F811
+    """An expanded out: every row would be written to one place, in no order."""
+    lib = B.load_library()
+    assert lib.blt_kv8_attend(_cache(B), _attn(B, **kw), None) == B.BLT_ERR_INVALID_ARG
+    assert b"overlap" in lib.blt_kv8_last_error()
+
+
+def test_rows_to_be_read_into_that_share_elements_are_refused(B):  # noqa: F811
+    lib = B.load_library()
+    for kw in (dict(row_stride=0), dict(head_stride=0), dict(head_stride=63), dict(row_stride=63)):
+        assert lib.blt_kv8_read(_cache(B), _rows(B, **kw), None) == B.BLT_ERR_INVALID_ARG, kw
+        assert b"overlap" in lib.blt_kv8_last_error()
