@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(kKv8SelThreads) k_kv8_select(const __grid_cons
         }
         dot += __shfl_xor_sync(0xffffffffu, dot, 1);
         dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-        // clamped to fp32's range, so that only pages that are always chosen have an infinite score
-        best = fmaxf(best, fminf(fmaxf((float)dot * qsc[g] * es[k], -FLT_MAX), FLT_MAX));
+        // The smaller scale first: what is in fp32's range stays there.  Clamped to that range, so that only pages that are
+        // always chosen have an infinite score.
+        best = fmaxf(best, fminf(fmaxf((float)dot * fminf(qsc[g], es[k]) * fmaxf(qsc[g], es[k]), -FLT_MAX), FLT_MAX));
       }
       if (t == 0 && p < nb) {
         if (p < a.n_sink || p >= nb - a.n_local) best = INFINITY;

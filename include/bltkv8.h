@@ -146,9 +146,10 @@ typedef struct {
 /* Choose pages for each row and key/value head by a bound on q.k: with the row's query head g in 8
  * bits (qi_c = round(q_c / 2^(eq - 127)), eq as an int8 block's e over the head's channels),
  *     score(page) = max over g of 2^(eq + k_sexp - 254) * sum_c max(qi_c k_min_c, qi_c k_max_c),
- * the sum in whole numbers.  Of the ceil(row_limit / page_tokens) visible pages the first n_sink and
- * the last n_local are chosen, then those with the highest scores (equal scores: the lower page
- * first) until n_select are; all of them if there are no more.  NaN in q counts as 0, infinities as
+ * the sum in whole numbers (a score beyond fp32's range counts as its end, one below it as 0).  Of
+ * the ceil(row_limit / page_tokens) visible pages the first n_sink and the last n_local are chosen,
+ * then those with the highest scores (equal scores: the lower page first) until n_select are; all of
+ * them if there are no more.  NaN in q counts as 0, infinities as
  * the largest code.  Needs summaries.  Errors: INVALID_ARG (max_pages above 49152), CUDA. */
 int blt_kv8_select(const blt_kv8_cache *c, const blt_kv8_selection *s, void *stream);
 
