@@ -31,6 +31,8 @@
 
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "kv8.cuh"
 
 namespace bltdec {
@@ -325,14 +327,14 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
     const int ex = max((int)(__float_as_uint(big) >> 23), 15);
-    const float up = kv8_pow2(268 - ex), down = kv8_pow2(ex - 14);
+    const float up = copysignf(kv8_pow2(268 - ex), a.scale), down = kv8_pow2(ex - 14);  // the sign of the scale with the query
 #pragma unroll
     for (int i = 0; i < KW; ++i) {
       kv8_planes<QP>(x[i][0] * up, x[i][1] * up, qf[n][i][0]);
       kv8_planes<QP>(x[i][2] * up, x[i][3] * up, qf[n][i][1]);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * (a.scale * 1.4426950408889634f);
+    for (int e = 0; e < 2; ++e) qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * (fabsf(a.scale) * 1.4426950408889634f);
   }
 
   float m[NQ][2], l[NQ][2], o[MT][NQ][4];
@@ -380,11 +382,16 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
       }
       const float ks = kv8_pow2(meta.y & 0xff);
       const bool whole = pos[u] + kKv8Block <= minlim;
+      float f[NQ][2];  // finite, so that a score of 0 stays 0
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) f[n][e] = fminf(ks * qs[n][e], FLT_MAX);
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sc[u][n][e] *= ks * qs[n][e & 1];
+          sc[u][n][e] = __fmul_rn(sc[u][n][e], f[n][e & 1]);  // rounded before it meets the maximum, which is
           if (!whole && pos[u] + g + (e >> 1) * 8 >= lim[n][e & 1]) sc[u][n][e] = -INFINITY;
         }
     }

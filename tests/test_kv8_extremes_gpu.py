@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from test_kv8_gpu import B, DT, Dev, check  # noqa: F401  (B: the fixture)
-from test_kv8_scales_gpu import stored
+from test_kv8_scales_gpu import KEYS, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +25,28 @@ def test_select_with_loud_queries_and_quiet_keys(B, D, qpow, kpow):  # noqa: F81
         want = c.select(0, q[r].double().cpu().numpy(), lim[r], 6, 1, 1)
         for h in range(2):
             assert sp[r, h, :int(sc[r, h])].tolist() == want[h], (r, h)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [60, 80, 100])
+@pytest.mark.parametrize("rows_", [3, 130])
+def test_scores_of_zero_between_loud_queries_and_keys(B, dt, power, rows_):  # noqa: F811
+    """Query and keys of 2^power in different channels: every score is 0, and a row gives the mean of what it sees."""
+    rng = np.random.default_rng(power)
+    n, D = 100, 64
+    k, v = np.zeros((n, 1, D)), rng.normal(size=(n, 1, D))
+    k[..., 1] = 2.0 ** power
+    c, d = stored(B, rng, "int8", 32, k, v)
+    q = torch.zeros(rows_, 1, D, dtype=DT[dt], device="cuda")
+    q[..., 0] = 2.0 ** power
+    lim = [1 + (7 * i) % n for i in range(rows_)]
+    values = c.keys(0, range(4))[1][0]
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+        for r in range(rows_):
+            seen = values[:lim[r]]
+            # weights are equal and exact; n + 64 roundings of sums of |v| / n, and the output's
+            tol = np.abs(seen).mean(0) * (n + 64) * 2.0 ** -23
+            want = seen.mean(0)
+            assert (np.abs(out[r, 0].double().cpu().numpy() - want) <= tol + (np.abs(want) + tol) * torch.finfo(DT[dt]).eps / 2).all()
+            assert abs(float(lse[r, 0]) - np.log(lim[r])) <= 2.0 ** -20
