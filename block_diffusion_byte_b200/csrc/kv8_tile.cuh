@@ -41,6 +41,9 @@ constexpr int kKvtLoaders = 3;                        // warps that convert, a t
 constexpr long long kKvtWaitClocks = 2000000000ll;    // about a second
 constexpr long long kKvtStallClocks = 20000000ll;     // where the waits are to run out
 constexpr float kKvtLargeScore = 1048576.f;           // 2^20 (log 2): half a step of fp32 is 2^-4 there
+// 2^-60: a product is at most 2^31, so that a score below this scale is 2^-29 at most and may as well be of this scale; and
+// scores of up to 2^67 are within fp32's range in its units
+constexpr float kKvtLeastScale = 8.673617379884035e-19f;
 constexpr float kKvtGrow = 6.f;                       // growth of the maximum (log 2) that is let stand
 constexpr int kKvtShift = 8;                          // weights are at most 2^(kKvtGrow + kKvtShift) < 65504
 // Least power of two that a weight is taken times: in f16 a weight (at most 2^kKvtGrow) rounds to 0 then, and l still has it.
@@ -303,11 +306,11 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
       for (int i = 0; i < N / 32; ++i) kvt_ld32(sp + i * 32, v[i]);
       const int4 meta = sm.meta[slot];
       const int pos0 = (j0 + j) * N;
-      // Scales of the blocks' scores.  A zero query or zero keys take them below fp32's range: kept above 0 (the scores are 0
-      // either way), so that a masked score, -inf, times it stays -inf; and finite, so that a score of 0 stays 0.
+      // Scales of the blocks' scores: at least kKvtLeastScale, as a zero query or zero keys take them below fp32's range, where
+      // a masked score, -inf, times it is NaN; and finite, so that a score of 0 stays 0.
       float ks[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) ks[b] = fminf(fmaxf(kv8_pow2(meta.x >> 8 * b & 255) * qs, FLT_MIN), FLT_MAX);
+      for (int b = 0; b < NB; ++b) ks[b] = fminf(fmaxf(kv8_pow2(meta.x >> 8 * b & 255) * qs, kKvtLeastScale), FLT_MAX);
       // A product is at most DH 2^15 top: no score of the tile is above kKvtLargeScore
       const bool small = kv8_pow2(meta.w >> 8) * qs <= kKvtLargeScore / (DH * 32768.f * (FMT == 0 ? 128.f : 512.f));
       const bool whole = __all_sync(0xffffffffu, pos0 + N <= lim && meta.z == 0 && small);

@@ -50,3 +50,25 @@ def test_scores_of_zero_between_loud_queries_and_keys(B, dt, power, rows_):  # n
             want = seen.mean(0)
             assert (np.abs(out[r, 0].double().cpu().numpy() - want) <= tol + (np.abs(want) + tol) * torch.finfo(DT[dt]).eps / 2).all()
             assert abs(float(lse[r, 0]) - np.log(lim[r])) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("top", [64.0, 96.0])
+@pytest.mark.parametrize("rows_", [3, 130])
+def test_zero_keys_beside_loud_ones_keep_their_weight(B, dt, top, rows_):  # noqa: F811
+    """A block of zero keys, one of keys of 2^20 that the query is orthogonal to, one with scores of 8 or 12: the zero keys
+    have weights of e^-8 or e^-12 beside them."""
+    rng = np.random.default_rng(3)
+    n, D = 64, 64
+    k, v = np.zeros((n, 1, D)), rng.normal(size=(n, 1, D))
+    k[16:32, :, 0] = 2.0 ** 20
+    k[32:48, :, 1] = top
+    k[48:, :, 1] = 1.0
+    v[:16] *= 2000.0
+    c, d = stored(B, rng, "int8", 32, k, v)
+    q = torch.zeros(rows_, 1, D, dtype=DT[dt], device="cuda")
+    q[..., 1] = 1.0
+    lim = [48 + i % 17 for i in range(rows_)]
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
+        check(c, q, out, lse, [0, rows_], lim, 0.125, dt)
