@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kKv8Warps * 32, kv8_ctas<DH, QP, NQ>()) k_kv8_
       kv8_planes<QP>(x[i][2] * up, x[i][3] * up, qf[n][i][1]);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * (fabsf(a.scale) * 1.4426950408889634f);
+    for (int e = 0; e < 2; ++e) qs[n][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4) * fabsf(a.scale) * 1.4426950408889634f;  // in this order: a scale near fp32's largest
   }
 
   float m[NQ][2], l[NQ][2], o[MT][NQ][4];

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kKvtThreads, kvt_smem<DH, QP>() <= 113 * 1024 
     }
     const int ex = max((int)(__float_as_uint(big) >> 23), 15);
     const float up = a.scale == 0.f ? 0.f : copysignf(kv8_pow2(268 - ex), a.scale);
-    const float qs = a.scale == 0.f ? 1.f : kv8_pow2(ex - 14) * (fabsf(a.scale) * 1.4426950408889634f);
+    const float qs = a.scale == 0.f ? 1.f : kv8_pow2(ex - 14) * fabsf(a.scale) * 1.4426950408889634f;  // in this order: a scale near fp32's largest
 #pragma unroll
     for (int c0 = 0; c0 < DH; c0 += QC) {
       if (nt == 0) break;  // the memory is the sums' at once

@@ -72,3 +72,18 @@ def test_zero_keys_beside_loud_ones_keep_their_weight(B, dt, top, rows_):  # noq
     for keys in KEYS:
         out, lse = d.attend(q, [0, rows_], lim, rows_, 0.125, max_keys=keys)
         check(c, q, out, lse, [0, rows_], lim, 0.125, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows_", [3, 130])
+@pytest.mark.parametrize("scale", [3e38, -3.4e38, 2e38])
+def test_scales_near_the_end_of_fp32(B, dt, rows_, scale):  # noqa: F811
+    rng = np.random.default_rng(5)
+    n, D = 130, 64
+    k, v = rng.normal(size=(2, n, 1, D))
+    c, d = stored(B, rng, "int8", 32, k * 1e-8, v)
+    q = torch.from_numpy(rng.normal(size=(rows_, 1, D)) * 1e-31).to(torch.float32).to(DT[dt]).cuda()
+    lim = [1 + (7 * i) % n for i in range(rows_)]
+    for keys in KEYS:
+        out, lse = d.attend(q, [0, rows_], lim, rows_, scale, max_keys=keys)
+        check(c, q, out, lse, [0, rows_], lim, float(np.float32(scale)), dt)
