@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_c
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
           const int gi = j * 32 + lane;
-          kv8_ld8(src, DT, (long long)(r0 + q0 + gi / GPR - start) * a.rs + (long long)h * a.hs + gi % GPR * 8, true, x[j]);
+          kv8_ld8(src, DT, (long long)(r0 + (q0 - start) + gi / GPR) * a.rs + (long long)h * a.hs + gi % GPR * 8, true, x[j]);
         }
       } else {
 #pragma unroll
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_append(const __grid_c
               x[j][e] = fabsf(y) > FLT_MAX && fabsf(x[j][e]) < (FMT == 0 ? 127.f : 448.f) ? copysignf(FLT_MAX, y) : y;
             }
           } else if (pos < end) {
-            kv8_ld8(src, DT, (long long)(r0 + pos - start) * a.rs + (long long)h * a.hs + ch, a.vec, x[j]);
+            kv8_ld8(src, DT, (long long)(r0 + (pos - start)) * a.rs + (long long)h * a.hs + ch, a.vec, x[j]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kKv8RowThreads, 4) k_kv8_read(const __grid_con
         kv8_decode8<FMT>(w[u], x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= kv8_pow2(e[u]);
-        kv8_st8(val ? a.v : a.k, DT, (long long)(r0 + q0 + gi / GPR - start) * a.rs + (long long)h * a.hs + gi % GPR * 8, a.vec, x);
+        kv8_st8(val ? a.v : a.k, DT, (long long)(r0 + (q0 - start) + gi / GPR) * a.rs + (long long)h * a.hs + gi % GPR * 8, a.vec, x);
       }
     }
   }
@@ -623,7 +623,7 @@ int store_or_read(const blt_kv8_cache* c, const blt_kv8_rows* rows, void* stream
   long long gy = c->n_heads;
   while (gy > 1 && px * c->batch * gy > 16ll * sm_count()) gy = (gy + 1) / 2;
   const dim3 grid((unsigned)px, (unsigned)gy, (unsigned)c->batch);
-  const int blocks = c->page_tokens / 16, touched = (a.max_rows + 30) / 16;
+  const int blocks = c->page_tokens / 16, touched = (int)((a.max_rows + 30ll) / 16);
   int warps = 2 * (blocks < touched ? blocks : touched);
   warps = warps < 4 ? 4 : warps > kKv8RowThreads / 32 ? kKv8RowThreads / 32 : warps;
   return store ? by_dim(c->head_dim, c->format, AppendLaunch{v, a, grid, warps * 32, (cudaStream_t)stream})

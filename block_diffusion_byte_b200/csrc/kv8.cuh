@@ -50,7 +50,7 @@ __device__ __forceinline__ int kv8_page(const Kv8View& c, int s, int pi) {
 __device__ __forceinline__ void kv8_rows_of(const int* off, int s, int n_rows, int max_rows, int* status, int& r0, int& r1) {
   r0 = __ldg(off + s);
   r1 = __ldg(off + s + 1);
-  const int a = min(max(r0, 0), n_rows), b = min(max(r1, a), min(n_rows, a + max_rows));
+  const int a = min(max(r0, 0), n_rows), b = min(max(r1, a), a + min(n_rows - a, max_rows));
   if ((a != r0 || b != r1) && status) set_status(status, kErrDevice);
   r0 = a;
   r1 = b;

@@ -87,3 +87,20 @@ def test_scales_near_the_end_of_fp32(B, dt, rows_, scale):  # noqa: F811
     for keys in KEYS:
         out, lse = d.attend(q, [0, rows_], lim, rows_, scale, max_keys=keys)
         check(c, q, out, lse, [0, rows_], lim, float(np.float32(scale)), dt)
+
+
+def test_append_from_the_end_of_a_long_array(B):  # noqa: F811
+    """Rows whose numbers are near 2^31: one row expanded over the array, so that it takes no memory."""
+    from _kv8_ref import Cache
+
+    n, rng = 2 ** 31 - 1, np.random.default_rng(6)
+    c = Cache("int8", 4, 1, 16, 32, [[2, 0], [3, 1]], rng)
+    d = Dev(B, c)
+    x = torch.from_numpy(rng.normal(size=(2, 1, 1, 32))).to(torch.float32).cuda()
+    k, v = (y.expand(n, 1, 32) for y in x)
+    # as many rows of a sequence as the array has are allowed for; there are 20 and 9
+    d.append(k, v, [n - 29, n - 9, n], [3, 5], n)
+    for s, (start, m) in enumerate(((3, 20), (5, 9))):
+        c.append(s, start, *(y[0].expand(m, 1, 32).double().cpu().numpy() for y in x))
+    d.same()
+    assert int(d.status) == 0
