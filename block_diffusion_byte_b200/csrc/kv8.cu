@@ -505,9 +505,20 @@ int check_rows(const blt_kv8_cache* c, const blt_kv8_rows* r, Kv8RowsArgs& a) {
   return BLT_OK;
 }
 
-// Rows to be written that share elements with the next row or head.
+// Whether two of the rows x heads pieces of `dim` elements that are to be written share an element: two offsets
+// i * row_stride + j * head_stride closer than dim.  Where one stride steps over the whole of the other axis, it is the other
+// one that counts; else each difference along the shorter axis is held against the nearest multiples of the other's stride.
 bool overlap(int rows, long long row_stride, int heads, long long head_stride, int dim) {
-  return (rows > 1 && row_stride < dim) || (heads > 1 && head_stride < dim);
+  if ((rows > 1 && row_stride < dim) || (heads > 1 && head_stride < dim)) return true;
+  if (rows <= 1 || heads <= 1 || row_stride / heads >= head_stride || head_stride / rows >= row_stride) return false;
+  const bool by_row = rows < heads;
+  const long long n = by_row ? rows : heads, step = by_row ? row_stride : head_stride;
+  const long long others = by_row ? heads : rows, other = by_row ? head_stride : row_stride;
+  for (long long i = 1; i < n; ++i) {
+    const long long k = i * step / other, d = i * step - k * other;
+    if ((k < others && d < dim) || (k + 1 < others && other - d < dim)) return true;
+  }
+  return false;
 }
 
 template <class F>

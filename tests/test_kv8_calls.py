@@ -110,3 +110,22 @@ def test_rows_to_be_read_into_that_share_elements_are_refused(B):  # noqa: F811
     for kw in (dict(row_stride=0), dict(head_stride=0), dict(head_stride=63), dict(row_stride=63)):
         assert lib.blt_kv8_read(_cache(B), _rows(B, **kw), None) == B.BLT_ERR_INVALID_ARG, kw
         assert b"overlap" in lib.blt_kv8_last_error()
+
+
+def share(rows, rs, heads, hs, dim):
+    at = sorted(i * rs + j * hs for i in range(rows) for j in range(heads))
+    return any(b - a < dim for a, b in zip(at, at[1:]))
+
+
+def test_rows_and_heads_that_share_elements_are_refused_and_no_others(B):  # noqa: F811
+    """Strides that are each wide enough, and rows that meet other rows' heads all the same; interleaved ones that do not."""
+    lib = B.load_library()
+    seen = {True: 0, False: 0}
+    for rows, heads in ((1, 2), (2, 2), (3, 2), (5, 4), (4, 8), (7, 6)):
+        for rs in (64, 96, 128, 160, 191, 192, 193, 256, 320, 384, 448, 512):
+            for hs in (64, 65, 96, 127, 128, 192, 200, 256, 448, 512):
+                want = share(rows, rs, heads, hs, 64)
+                lib.blt_kv8_attend(_cache(B), _attn(B, n_rows=rows, max_rows=rows, n_q_heads=heads, out_row_stride=rs, out_head_stride=hs), None)
+                assert (b"overlap" in lib.blt_kv8_last_error()) == want, (rows, rs, heads, hs)
+                seen[want] += 1
+    assert min(seen.values()) > 50
