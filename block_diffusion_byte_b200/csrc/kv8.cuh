@@ -69,7 +69,7 @@ __device__ __forceinline__ int kv8_exponent(float amax) {
   return max(e, kKv8LowExp);
 }
 
-// x with infinities as the largest float and NaN as 0.
+// x with NaN as 0; infinities are left to the caller's clamp.
 __device__ __forceinline__ float kv8_finite(float x) {
   return x != x ? 0.f : x;
 }

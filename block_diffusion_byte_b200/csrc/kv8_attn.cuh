@@ -21,12 +21,16 @@
 // Warps are joined in shared memory, and the CTAs that split a long key axis (a cluster) over distributed
 // shared memory, in a fixed order: no workspace, no second launch, no atomics.
 //
-// Bound by memory at long contexts: 64 sequences of 4096 to 8192 keys, 8 heads of 128, four query heads each, e4m3: 150 us,
-// 5.4 TB/s (0.82 of the measured copy rate); the rest is uneven ends and the dependent work of a warp's step (about 340
-// instructions for 16 keys).  By the chain of lookups at its start (row range, limit, page, exponents: about 4 us) when
-// short: 4 rows at 1028 keys, 16 heads of 64, fp32: 6.8 us; one row at 8192: 12.7 us.  Steps on the way, on the 64
-// sequences: codes as bf16 with the next step in registers, one CTA an SM 282 us; f16 and the ring 171 us; queries
-// loaded at once 164 us; pieces moved off shared banks 158 us; keys in halves 150 us.
+// The tensor cores cut sums to fp32 where they do not round them; a warp's chain of products is short (keys / 16 / warps / CTAs
+// of the cluster), and fp32 outputs are 4e-7 off at 1028 keys, 8e-7 at 1024 selected ones (plain fp32: 4e-7, 5e-7).
+//
+// Bound by memory at long contexts: 64 sequences of 4096 to 8192 keys, 8 heads of 128, four query heads each, e4m3: 154 to
+// 172 us with the lengths drawn, 5.2 TB/s (0.79 of the measured copy rate); the rest is uneven ends and the dependent work
+// of a warp's step (about 340 instructions for 16 keys).  By the chain of lookups at its start (row range, limit, page,
+// exponents: about 4 us) when short: 4 rows at 1028 keys, 16 heads of 64, fp32: 6.9 us; one row at 8192: 12.7 us.  Steps on
+// the way, on the 64 sequences of one draw: codes as bf16 with the next step in registers, one CTA an SM 282 us; f16 and the
+// ring 171 us; queries loaded at once 164 us; pieces moved off shared banks 158 us; keys in halves 150 us; value scales as
+// each query sees them 153 us; finite factors 154 us.
 #pragma once
 
 #include <cooperative_groups.h>

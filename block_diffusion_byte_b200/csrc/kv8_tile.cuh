@@ -20,11 +20,12 @@
 // Bound by the weights' work: one exponential each on the 16-a-clock unit (512 clocks a tile) and, in a thread, the chain
 // score -> maximum -> exponential -> f16 -> tensor memory (about 1000 clocks a tile and CTA, two CTAs an SM); the
 // products take 350 clocks a tile (one f16 plane each) and never wait.  Four causal prompts of 2048, 16 heads of 64, bf16:
-// 98 us, 351 TFLOP/s; 1024 fp32 rows at 8192 keys (two planes of q and of the weights): 105 us, 306 TFLOP/s.  Steps on
+// 100 us, 344 TFLOP/s; 1024 fp32 rows at 8192 keys (two planes of q and of the weights): 111 us, 290 TFLOP/s.  Steps on
 // the way (the two in turn): 128-key tiles, S and P in one place 195, 327 us; masked and whole tiles apart 123, 186;
 // 64-key tiles with the next tile's S under this one's weights 105, 146; bulk copies converted in place, a warp a tile,
 // three S tiles 95, 132 (with one barrier for the weights of all tiles, which was wrong; 100 with one a tile); keys split
-// over a cluster where tiles are few -, 100; fp32 sums in chains of 8 tiles -, 105.
+// over a cluster where tiles are few -, 100; fp32 sums in chains of 8 tiles -, 105; scales of blocks in the scores and weights
+// instead of the operands, scores of any size 100, 111.
 #pragma once
 
 #include <cfloat>
@@ -53,8 +54,10 @@ constexpr int kKvtN = 64;                             // keys a tile
 // Tiles of operands in shared memory: four and two CTAs an SM, or one CTA where a tile takes 32 KB.
 template <int DH, int QP>
 __host__ __device__ constexpr int kvt_slots() { return DH > 64 && QP == 1 ? 5 : 4; }
-// The tensor cores cut each sum to fp32 instead of rounding it, so a long chain of products drifts (8e-6 of fp32 outputs
-// at 4096 keys).  fp32 rows end the chain after this many tiles and add it to a total with rounding (1e-6); 0: one chain.
+// The tensor cores cut each sum to fp32 instead of rounding it, so a long chain of products drifts (fp32 outputs at 8192
+// keys: 8.2e-6 off).  fp32 rows end the chain after this many tiles and add it to a total with rounding (1.7e-6, plain fp32
+// 1.7e-6); 0: one chain, for bf16 and f16 rows, whose own rounding is up to 2^-9 and 2^-12 of a number (the drift grows with
+// the keys: at this rate it is that of f16 at about 200000).
 template <int QP>
 __host__ __device__ constexpr int kvt_fold() { return QP == 2 ? 8 : 0; }
 template <int DH, int QP>

@@ -111,8 +111,10 @@ typedef struct {
 #define BLT_FLAG_KV8_E4M3 32 /* head, or e4m3 codes.  One of the two at most; head dim 32, 64 or 128, page_tokens <= 256.
                                 K/V then take a half (bf16 weights) or a quarter (fp32) of their bytes.  Every pass runs on
                                 the per-phase kernels (BLT_FLAG_PERSISTENT is ignored) and blt_dec_prefill_noalloc is
-                                refused.  A cached position can lose low bits when rows that share its 16 positions are
-                                stored later (drafts and block rows included): see blt_kv8_append. */
+                                refused: one sequence decodes slower than on the persistent kernel, many long ones
+                                faster.  The handle keeps no page summaries (blt_kv8_select).  A cached position can
+                                lose low bits when rows that share its 16 positions are stored later (drafts and block
+                                rows included): see blt_kv8_append. */
 
 typedef struct {
   const float *embed;      /* host [vocab, d] */

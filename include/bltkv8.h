@@ -112,11 +112,11 @@ typedef struct {
   const int32_t *row_limit;   /* [n_rows] row r attends positions 0 .. row_limit[r] - 1 of its sequence */
   /* Selected pages, or NULL for all: row r, head h attends only the positions < row_limit[r] in pages
    * (indices into its sequence's page_table row) sel_pages[(r * n_heads + h) * n_select ..], the first
-   * sel_count[r * n_heads + h] of them, in increasing order; an entry that is negative or not greater
-   * than the one before it is ignored. */
+   * sel_count[r * n_heads + h] of them, in increasing order; an entry that is negative, at least
+   * max_pages or not greater than the one before it is ignored. */
   const int32_t *sel_pages, *sel_count;
   int32_t n_select;
-  int32_t flags; /* 0 */
+  int32_t flags; /* 0, or BLT_KV8_TEST_STALL */
 } blt_kv8_attention;
 
 #define BLT_KV8_TEST_STALL 1 /* test only: in a call of many rows, the keys for the first sequence's last tile of 128
@@ -126,7 +126,10 @@ typedef struct {
  * lse -inf.  Sums, maxima and products accumulate in fp32; fp32 q is used to 22 bits, and weights
  * enter the value product with 22 (F32, F16) or 11 (BF16) bits.  Cut are channels of q 2^32 below the
  * row's largest, and weights times their block's value scale 2^32 below the largest value scale among
- * the blocks that the row sees; keys and values that a row does not see take nothing from it.
+ * the blocks that the row sees; keys and values that a row does not see take nothing from it.  The
+ * tensor cores cut sums to fp32 where they do not round them, so an output over n keys can be off by
+ * n / 4 + 64 steps of 2^-23 of its sum of magnitudes; for F32 and many rows they are cut over 512 keys
+ * at a time and rounded in between.  Scores have to lie in fp32's range.
  * Positions below row_limit have to be stored.  The same call gives the same bits; the order of the
  * sums, and with it the last bits, depends on max_rows, max_keys, batch and the limits of the rows
  * that share a tile.  n_rows = 0 or max_rows = 0: nothing is done.
@@ -143,14 +146,16 @@ typedef struct {
   int32_t *sel_pages, *sel_count; /* as in blt_kv8_attention, unused entries -1 */
 } blt_kv8_selection;
 
-/* Choose pages for each row and key/value head by a bound on q.k: with the row's query head g in 8
- * bits (qi_c = round(q_c / 2^(eq - 127)), eq as an int8 block's e over the head's channels),
+/* Choose pages for each row and key/value head by an estimate of the largest q.k: with the row's query
+ * head g in 8 bits (qi_c = round(q_c / 2^(eq - 127)), eq as an int8 block's e over the head's channels),
  *     score(page) = max over g of 2^(eq + k_sexp - 254) * sum_c max(qi_c k_min_c, qi_c k_max_c),
  * the sum in whole numbers (a score beyond fp32's range counts as its end, one below it as 0).  Of
  * the ceil(row_limit / page_tokens) visible pages the first n_sink and the last n_local are chosen,
  * then those with the highest scores (equal scores: the lower page first) until n_select are; all of
- * them if there are no more.  NaN in q counts as 0, infinities as
- * the largest code.  Needs summaries.  Errors: INVALID_ARG (max_pages above 49152), CUDA. */
+ * them if there are no more.  q and the summaries are rounded to nearest, so a page's largest q.k can
+ * exceed its score: by half a step of q times the sum of the page's largest magnitudes, and half a step
+ * of k_sexp times the sum of |q|.  NaN in q counts as 0, infinities as the largest code.  Needs
+ * summaries.  Errors: INVALID_ARG (max_pages above 49152), CUDA. */
 int blt_kv8_select(const blt_kv8_cache *c, const blt_kv8_selection *s, void *stream);
 
 /* Message of this thread's last failed blt_kv8_* call ("" if none). */
